@@ -13,6 +13,7 @@ from ._lib import (  # noqa: F401
     SHUFFLE_K,
     SHUFFLE_N,
     last_error,
+    layer_last_error,
     load,
     plan,
 )
@@ -39,4 +40,20 @@ from .ops import (  # noqa: F401
     f8f8bf16_quantize_rowwise,
     f8f8bf16_rowwise_grouped_stacked_preshuffle,
     f8f8bf16_shuffle_b,
+)
+from .layer import (  # noqa: F401
+    RmsNorm,
+    Route,
+    SiluMul,
+    f8f8bf16_k_offsets_capacity,
+    f8f8bf16_moe_combine,
+    f8f8bf16_moe_combine_backward,
+    f8f8bf16_moe_dispatch,
+    f8f8bf16_quantize_k_offsets,
+    f8f8bf16_rmsnorm_backward,
+    f8f8bf16_rmsnorm_quantize,
+    f8f8bf16_route,
+    f8f8bf16_route_backward,
+    f8f8bf16_silu_mul_backward,
+    f8f8bf16_silu_mul_quantize,
 )

@@ -1,4 +1,5 @@
-"""ctypes loader for libfp8gg.so (the C ABI declared in include/fp8gg.h)."""
+"""ctypes loader for libfp8gg.so (the C ABI declared in include/fp8gg.h and
+include/fp8gg_layer.h)."""
 from __future__ import annotations
 
 import ctypes
@@ -47,6 +48,31 @@ EXPORTS = (
     "f8f8bf16_plan",
     "f8f8bf16_num_configs",
 )
+
+# Every symbol include/fp8gg_layer.h declares.
+LAYER_EXPORTS = (
+    "f8f8bf16_rmsnorm_quantize",
+    "f8f8bf16_rmsnorm_backward",
+    "f8f8bf16_rmsnorm_backward_workspace",
+    "f8f8bf16_route",
+    "f8f8bf16_route_workspace",
+    "f8f8bf16_route_backward",
+    "f8f8bf16_moe_dispatch",
+    "f8f8bf16_moe_combine",
+    "f8f8bf16_moe_combine_backward",
+    "f8f8bf16_silu_mul_quantize",
+    "f8f8bf16_silu_mul_backward",
+    "f8f8bf16_quantize_k_offsets",
+    "f8f8bf16_quantize_k_offsets_workspace",
+    "f8f8bf16_k_offsets_capacity",
+    "f8f8bf16_layer_last_error",
+)
+
+DTYPE_BF16 = 0
+DTYPE_F32 = 1
+DTYPE_E4M3 = 2
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
 
 
 class Plan(ctypes.Structure):
@@ -118,6 +144,24 @@ def load() -> ctypes.CDLL:
     lib.f8f8bf16_plan.restype = I
     lib.f8f8bf16_num_configs.argtypes = []
     lib.f8f8bf16_num_configs.restype = I32
+    F = ctypes.c_float
+    lib.f8f8bf16_rmsnorm_quantize.argtypes = [P, P, P, I, F, I, P, P, P, P, P, I64, I64, P]
+    lib.f8f8bf16_rmsnorm_backward.argtypes = [P, P, P, I, P, P, P, P, P, I64, I64, I64, P]
+    lib.f8f8bf16_rmsnorm_backward_workspace.argtypes = [I64, I64]
+    lib.f8f8bf16_route.argtypes = [P, I, P, I, I64, I64, I, I, F, P, P, P, P, P, I64, I64, I64, I64, P]
+    lib.f8f8bf16_route_workspace.argtypes = [I64, I64, I64]
+    lib.f8f8bf16_route_backward.argtypes = [P, I, P, P, I, I, F, P, I64, I64, I64, P]
+    lib.f8f8bf16_moe_dispatch.argtypes = [P, P, I64, P, P, P, I64, I64, I64, I64, P]
+    lib.f8f8bf16_moe_combine.argtypes = [P, P, P, P, P, I64, I64, I64, I64, P]
+    lib.f8f8bf16_moe_combine_backward.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, P]
+    lib.f8f8bf16_silu_mul_quantize.argtypes = [P, I, P, P, P, P, I64, I64, P]
+    lib.f8f8bf16_silu_mul_backward.argtypes = [P, P, P, P, I64, I64, P]
+    lib.f8f8bf16_quantize_k_offsets.argtypes = [P, I, P, I64, P, P, P, P, P, I64, I64, I64, I64, P]
+    lib.f8f8bf16_quantize_k_offsets_workspace.argtypes = [I64, I64, I64]
+    lib.f8f8bf16_k_offsets_capacity.argtypes = [I64, I64]
+    for name in LAYER_EXPORTS:
+        getattr(lib, name).restype = I64 if name.endswith(("_workspace", "_capacity")) else I
+    lib.f8f8bf16_layer_last_error.restype = ctypes.c_char_p
     _lib = lib
     return lib
 
@@ -130,6 +174,19 @@ def check(status: int, what: str) -> None:
     if status == OK:
         return
     msg = f"{what}: {last_error()}"
+    if status in (ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED_SHAPE):
+        raise ValueError(msg)
+    raise RuntimeError(msg)
+
+
+def layer_last_error() -> str:
+    return load().f8f8bf16_layer_last_error().decode()
+
+
+def layer_check(status: int, what: str) -> None:
+    if status == OK:
+        return
+    msg = f"{what}: {layer_last_error()}"
     if status in (ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED_SHAPE):
         raise ValueError(msg)
     raise RuntimeError(msg)

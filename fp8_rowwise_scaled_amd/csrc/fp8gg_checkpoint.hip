@@ -1,0 +1,381 @@
+// 8-bit activation checkpoints (gfx950): the gated activation with its fp8 output and
+// the checkpoint of its input, its gradient from the checkpoint, and the weight
+// gradient's operand (rows requantised per group and column, transposed).
+//
+// The checkpoint keeps the input of the gated activation as e4m3 codes with one scale
+// per row, half and 128 columns: 1.03 bytes per value where bf16 takes 2.  The forward
+// pass reads H once: a wave's 16 lanes x 8 columns are one scale block, so the block's
+// largest magnitude is a reduction over 16 lanes; the activation itself stays in
+// registers until the row's largest magnitude is known.  The backward pass is
+// elementwise.  All are bound by HBM.
+#include "fp8gg_layer_internal.h"
+
+namespace fp8gg {
+
+namespace {
+
+constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+// 1 / (1 + exp(-g)) from the hardware's exp2 and reciprocal (a few units in the last
+// place plus |g| 2^-23; what it feeds is rounded to 8 or 16 bits).
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
+}
+
+// A team of TPR threads works on one row, NV x 8 columns of each half per thread.
+template <int TPR, int NV, bool BLOCKED>
+__global__ void __launch_bounds__(threads_of(TPR)) silu_mul_quantize_kernel(SiluArgs a) {
+  constexpr int kTeams = threads_of(TPR) / TPR;
+  __shared__ uint32_t mosts[2][threads_of(TPR) / 64];
+  const int lane = threadIdx.x % TPR;
+  const int nvec = a.I / 8, nblocks = (a.I + 127) / 128;
+  int slot = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kTeams + threadIdx.x / TPR; row < a.rows;
+       row += (int64_t)gridDim.x * kTeams) {
+    u32x4 rg[NV], ru[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = i * TPR + lane;
+      rg[i] = ru[i] = u32x4{0, 0, 0, 0};
+      if (j < nvec) {
+        rg[i] = reinterpret_cast<const u32x4*>(a.H)[2 * row * nvec + j];
+        ru[i] = reinterpret_cast<const u32x4*>(a.H)[(2 * row + 1) * nvec + j];
+      }
+    }
+    F8 act[NV];
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = i * TPR + lane;
+      const F8 g = unpack_bf16(rg[i]), u = unpack_bf16(ru[i]);
+      if (a.HQ) {
+        const float ag = __uint_as_float(row16_reduce(mag_max(g, 0), MaxU()));
+        const float au = __uint_as_float(row16_reduce(mag_max(u, 0), MaxU()));
+        if (j < nvec) {
+          reinterpret_cast<u32x2*>(a.HQ)[2 * row * nvec + j] = codes_of(g, inverse_scale(ag));
+          reinterpret_cast<u32x2*>(a.HQ)[(2 * row + 1) * nvec + j] = codes_of(u, inverse_scale(au));
+          if ((lane & 15) == 0) {
+            a.h_scale[2 * row * nblocks + j / 16] = scale_of(ag);
+            a.h_scale[(2 * row + 1) * nblocks + j / 16] = scale_of(au);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) act[i].v[e] = g.v[e] * sigmoid(g.v[e]) * u.v[e];
+      if constexpr (BLOCKED) {
+        const float amax = __uint_as_float(row16_reduce(mag_max(act[i], 0), MaxU()));
+        if (j < nvec) {
+          reinterpret_cast<u32x2*>(a.AQ)[row * nvec + j] = codes_of(act[i], inverse_scale(amax));
+          if ((lane & 15) == 0) a.a_scale[row * nblocks + j / 16] = scale_of(amax);
+        }
+      } else {
+        most = mag_max(act[i], most);
+      }
+    }
+    if constexpr (!BLOCKED) {
+      most = wave_reduce(most, MaxU());
+      if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) mosts[slot][threadIdx.x >> 6] = most;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) most = umax(most, mosts[slot][w]);
+        slot ^= 1;   // rewritten only after the next row's barrier
+      }
+      const float amax = __uint_as_float(most), inv = inverse_scale(amax);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int j = i * TPR + lane;
+        if (j < nvec) reinterpret_cast<u32x2*>(a.AQ)[row * nvec + j] = codes_of(act[i], inv);
+      }
+      if (lane == 0) a.a_scale[row] = scale_of(amax);
+    }
+  }
+}
+
+// TX threads along the row (eight columns each), 256 / TX rows per workgroup.
+template <int TX>
+__global__ void __launch_bounds__(256) silu_mul_backward_kernel(SiluBackwardArgs a, int chunks, int64_t work) {
+  constexpr int kRows = 256 / TX;
+  const int nvec = a.I / 8, nblocks = (a.I + 127) / 128;
+  for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
+    const int64_t rows = i / chunks;
+    const int64_t row = rows * kRows + threadIdx.x / TX;
+    const int j = (int)(i - rows * chunks) * TX + threadIdx.x % TX;
+    if (row >= a.rows || j >= nvec) continue;
+    const F8 da = unpack_bf16(reinterpret_cast<const u32x4*>(a.dA)[row * nvec + j]);
+    const F8 qg = values_of(reinterpret_cast<const u32x2*>(a.HQ)[2 * row * nvec + j]);
+    const F8 qu = values_of(reinterpret_cast<const u32x2*>(a.HQ)[(2 * row + 1) * nvec + j]);
+    const float sg = a.h_scale[2 * row * nblocks + j / 16];
+    const float su = a.h_scale[(2 * row + 1) * nblocks + j / 16];
+    F8 dg, du;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float g = qg.v[e] * sg, s = sigmoid(g), silu = g * s;
+      du.v[e] = da.v[e] * silu;
+      // sig (1 + g (1 - sig)) = sig + silu (1 - sig)
+      dg.v[e] = da.v[e] * (qu.v[e] * su) * __builtin_fmaf(silu, 1.0f - s, s);
+    }
+    reinterpret_cast<u32x4*>(a.dH)[2 * row * nvec + j] = pack_bf16(dg);
+    reinterpret_cast<u32x4*>(a.dH)[(2 * row + 1) * nvec + j] = pack_bf16(du);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The weight gradient's operand
+// ---------------------------------------------------------------------------
+//
+// Rows are cut into chunks of at most 128 rows of one group.  The first kernel writes
+// each chunk's largest magnitude per column; the second one joins the chunks of the
+// group, requantises its own 128 rows x 128 columns and turns them through LDS, so that
+// both sides are accessed in runs of at least 128 bytes.  The rows are read twice; the
+// second time the Infinity Cache holds them unless they pass 256 MB.
+
+constexpr int kTile = 128;             // columns of the second kernel's tile
+constexpr int kLdsStride = 33;         // words per column: 128 codes and one of padding
+
+struct Chunk {
+  int group;         // -1: past the last chunk
+  int rows;          // rows of the chunk
+  int first;         // first chunk of its group
+  int chunks;        // chunks of its group
+  int64_t row;       // first row in X
+  int64_t col;       // first column in XT
+  int64_t last;      // one past the group's last column (a multiple of 16)
+};
+
+// Finds chunk c; every wave of the workgroup does so by itself.  Counts are clamped as
+// in the stacked layout: negative ones to 0, ends to R.
+__device__ __forceinline__ Chunk find_chunk(const KOffsetsArgs& a, int c) {
+  const int lane = threadIdx.x & 63;
+  Chunk f{-1, 0, 0, 0, 0, 0, 0};
+  int64_t rows_before = 0, cols_before = 0;
+  int chunks_before = 0;
+  for (int g0 = 0; g0 < a.G; g0 += 64) {
+    int64_t m = g0 + lane < a.G ? a.M_sizes[g0 + lane] : 0;
+    m = m < 0 ? 0 : (m > a.R ? a.R : m);
+    int64_t end = m;
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t y = __shfl_up(end, off, 64);
+      if (lane >= off) end += y;
+    }
+    end += rows_before;
+    int64_t begin = end - m;
+    begin = begin > a.R ? a.R : begin;
+    end = end > a.R ? a.R : end;
+    const int64_t size = end - begin;
+    const int n = (int)((size + kChunkRows - 1) / kChunkRows);
+    const int64_t cols = (size + 15) / 16 * 16;
+    int n_end = n;
+    int64_t cols_end = cols;
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(n_end, off, 64);
+      const int64_t z = __shfl_up(cols_end, off, 64);
+      if (lane >= off) {
+        n_end += y;
+        cols_end += z;
+      }
+    }
+    n_end += chunks_before;
+    cols_end += cols_before;
+    const uint64_t hit = __ballot(c >= n_end - n && c < n_end);
+    if (hit) {
+      const int src = __ffsll((unsigned long long)hit) - 1;
+      f.group = g0 + src;
+      f.chunks = __shfl(n, src, 64);
+      f.first = __shfl(n_end, src, 64) - f.chunks;
+      const int64_t begins = __shfl(begin, src, 64), ends = __shfl(end, src, 64);
+      f.last = __shfl(cols_end, src, 64);
+      f.row = begins + (int64_t)(c - f.first) * kChunkRows;
+      f.rows = (int)(ends - f.row < kChunkRows ? ends - f.row : kChunkRows);
+      f.col = f.last - __shfl(cols, src, 64) + (int64_t)(c - f.first) * kChunkRows;
+      return f;
+    }
+    rows_before = __shfl(end, 63, 64);
+    chunks_before = __shfl(n_end, 63, 64);
+    cols_before = __shfl(cols_end, 63, 64);
+  }
+  f.last = cols_before;
+  return f;
+}
+
+// E4M3: 16 codes per thread and load, else 8 bf16 values.
+template <bool E4M3>
+__device__ __forceinline__ void load_values(const KOffsetsArgs& a, int64_t row, int col, float* v) {
+  if constexpr (E4M3) {
+    const u32x4 q = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(a.X) + row * a.K + col);
+    const float s = a.x_scale[row * a.scale_cols + (a.scale_cols > 1 ? col / 128 : 0)];
+    const F8 lo = values_of(u32x2{q[0], q[1]}), hi = values_of(u32x2{q[2], q[3]});
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = lo.v[e] * s;
+      v[8 + e] = hi.v[e] * s;
+    }
+  } else {
+    const F8 f = unpack_bf16(*reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.X) + row * a.K + col));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = f.v[e];
+  }
+}
+
+// partial[c][k]: largest magnitude of column k in chunk c.  512 columns per workgroup;
+// its rows of lanes take every 4th (bf16) or 8th (codes) row.
+template <bool E4M3>
+__global__ void __launch_bounds__(256) column_amax_kernel(KOffsetsArgs a, int tiles) {
+  constexpr int W = E4M3 ? 16 : 8;
+  constexpr int kLanes = 512 / W, kRows = 256 / kLanes;
+  __shared__ uint32_t most[kRows][512 + 4];
+  const int chunk = blockIdx.x / tiles, col0 = (int)(blockIdx.x % tiles) * 512;
+  const Chunk f = find_chunk(a, chunk);
+  if (f.group < 0) return;
+  const int lx = threadIdx.x % kLanes, ly = threadIdx.x / kLanes;
+  const int col = col0 + lx * W;
+  uint32_t m[W] = {};
+  if (col < a.K) {
+    for (int r = ly; r < f.rows; r += kRows) {
+      float v[W];
+      load_values<E4M3>(a, f.row + r, col, v);
+#pragma unroll
+      for (int e = 0; e < W; ++e) m[e] = umax(m[e], mag(v[e]));
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < W; ++e) most[ly][lx * W + e] = m[e];
+  __syncthreads();
+  for (int x = threadIdx.x; x < 512; x += 256) {
+    if (col0 + x >= a.K) break;
+    uint32_t top = most[0][x];
+#pragma unroll
+    for (int y = 1; y < kRows; ++y) top = umax(top, most[y][x]);
+    a.partial[(int64_t)chunk * a.K + col0 + x] = __uint_as_float(top);
+  }
+}
+
+// After the chunks comes one more row of workgroups, which writes k_offsets, the scales
+// of empty groups and the columns past the last group.
+template <bool E4M3>
+__global__ void __launch_bounds__(256) transpose_quantize_kernel(KOffsetsArgs a, int tiles, int chunks) {
+  constexpr int W = E4M3 ? 16 : 8;
+  constexpr int kLanes = kTile / W, kRowLanes = 256 / kLanes;
+  __shared__ uint32_t turned[kTile * kLdsStride];
+  __shared__ float inverse[kTile];
+  const int chunk = blockIdx.x / tiles, col0 = (int)(blockIdx.x % tiles) * kTile;
+  if (chunk == chunks) {
+    const Chunk f = find_chunk(a, 0x7FFFFFFF);
+    const int64_t tail = (a.cap - f.last) / 16;
+    for (int64_t i = threadIdx.x; i < tail * kTile; i += 256) {
+      const int k = col0 + (int)(i / tail);
+      if (k < a.K) *reinterpret_cast<u32x4*>(a.XT + k * a.cap + f.last + (i % tail) * 16) = u32x4{0, 0, 0, 0};
+    }
+    int64_t row = 0, col = 0;
+    for (int g = 0; g < a.G; ++g) {
+      int64_t m = a.M_sizes[g];
+      m = m < 0 ? 0 : (m > a.R - row ? a.R - row : m);
+      row += m;
+      col += (m + 15) / 16 * 16;
+      if (m == 0 && (int)threadIdx.x < kTile && col0 + (int)threadIdx.x < a.K)
+        a.t_scale[(int64_t)g * a.K + col0 + threadIdx.x] = 1.f;
+      if (col0 == 0 && threadIdx.x == 0) a.k_offsets[g] = (int32_t)col;
+    }
+    return;
+  }
+  const Chunk f = find_chunk(a, chunk);
+  if (f.group < 0) return;
+  if (threadIdx.x < kTile) {
+    const int k = col0 + threadIdx.x;
+    uint32_t m = 0;
+    if (k < a.K)
+      for (int c = f.first; c < f.first + f.chunks; ++c) m = umax(m, __float_as_uint(a.partial[(int64_t)c * a.K + k]));
+    const float amax = __uint_as_float(m);
+    inverse[threadIdx.x] = inverse_scale(amax);
+    if (k < a.K && chunk == f.first) a.t_scale[(int64_t)f.group * a.K + k] = scale_of(amax);
+  }
+  __syncthreads();
+  const int lx = threadIdx.x % kLanes, ly = threadIdx.x / kLanes;
+  const int col = col0 + lx * W;
+  float inv[W];
+#pragma unroll
+  for (int e = 0; e < W; ++e) inv[e] = inverse[lx * W + e];
+  // four neighbouring rows per thread: their codes of one column are one LDS word
+  for (int r = ly * 4; r < kChunkRows; r += kRowLanes * 4) {
+    float v[4][W] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r + i < f.rows && col < a.K) load_values<E4M3>(a, f.row + r + i, col, v[i]);
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[0][e] * inv[e], v[1][e] * inv[e], 0, false);
+      q = __builtin_amdgcn_cvt_pk_fp8_f32(v[2][e] * inv[e], v[3][e] * inv[e], q, true);
+      turned[(lx * W + e) * kLdsStride + r / 4] = (uint32_t)q;
+    }
+  }
+  __syncthreads();
+  const int runs = (f.rows + 15) / 16;
+  for (int i = threadIdx.x; i < kTile * 8; i += 256) {
+    const int k = i / 8, s = i % 8;
+    if (col0 + k < a.K && s < runs) {
+      const uint32_t* w = turned + k * kLdsStride + s * 4;
+      *reinterpret_cast<u32x4*>(a.XT + (col0 + k) * a.cap + f.col + s * 16) = u32x4{w[0], w[1], w[2], w[3]};
+    }
+  }
+}
+
+template <int TPR, int NV>
+hipError_t launch_silu(const SiluArgs& a, int block, hipStream_t stream) {
+  constexpr int kTeams = threads_of(TPR) / TPR;
+  const int64_t want = (a.rows + kTeams - 1) / kTeams;
+  const dim3 grid((uint32_t)(want < 65536 ? want : 65536)), threads(threads_of(TPR));
+  if (block) hipLaunchKernelGGL((silu_mul_quantize_kernel<TPR, NV, true>), grid, threads, 0, stream, a);
+  else hipLaunchKernelGGL((silu_mul_quantize_kernel<TPR, NV, false>), grid, threads, 0, stream, a);
+  return hipGetLastError();
+}
+
+template <int TX>
+hipError_t launch_silu_back(const SiluBackwardArgs& a, hipStream_t stream) {
+  const int chunks = (a.I / 8 + TX - 1) / TX;
+  const int64_t work = (a.rows + 256 / TX - 1) / (256 / TX) * chunks;
+  hipLaunchKernelGGL((silu_mul_backward_kernel<TX>), dim3((uint32_t)(work < (1 << 20) ? work : (1 << 20))), dim3(256), 0,
+                     stream, a, chunks, work);
+  return hipGetLastError();
+}
+
+template <bool E4M3>
+hipError_t launch_k_offsets(const KOffsetsArgs& a, hipStream_t stream) {
+  const int chunks = (int)k_offsets_chunks(a.R, a.G);
+  if (chunks > 0) {
+    const int tiles = (a.K + 511) / 512;
+    hipLaunchKernelGGL((column_amax_kernel<E4M3>), dim3(chunks * tiles), dim3(256), 0, stream, a, tiles);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int tiles = (a.K + kTile - 1) / kTile;
+  hipLaunchKernelGGL((transpose_quantize_kernel<E4M3>), dim3((chunks + 1) * tiles), dim3(256), 0, stream, a, tiles,
+                     chunks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_silu_mul_quantize(const SiluArgs& a, int block, hipStream_t stream) {
+  if (a.rows == 0) return hipSuccess;
+  const int nvec = a.I / 8;
+  if (nvec <= 64) return launch_silu<64, 1>(a, block, stream);
+  if (nvec <= 256) return launch_silu<256, 1>(a, block, stream);
+  if (nvec <= 512) return launch_silu<256, 2>(a, block, stream);
+  if (nvec <= 1024) return launch_silu<256, 4>(a, block, stream);
+  return launch_silu<1024, 4>(a, block, stream);
+}
+
+hipError_t launch_silu_mul_backward(const SiluBackwardArgs& a, hipStream_t stream) {
+  if (a.rows == 0) return hipSuccess;
+  const int nvec = a.I / 8;
+  if (nvec <= 64) return launch_silu_back<64>(a, stream);
+  if (nvec <= 128) return launch_silu_back<128>(a, stream);
+  return launch_silu_back<256>(a, stream);
+}
+
+hipError_t launch_quantize_k_offsets(const KOffsetsArgs& a, hipStream_t stream) {
+  if (a.K == 0 || a.G == 0) return hipSuccess;
+  return a.x_scale ? launch_k_offsets<true>(a, stream) : launch_k_offsets<false>(a, stream);
+}
+
+}  // namespace fp8gg

@@ -1,0 +1,291 @@
+// Root-mean-square norm with the residual's addition and an fp8 output, and its
+// gradient (gfx950).
+//
+// Forward.  With h = bf16(x + residual), y = h rstd w and q = y / (amax|y| / 448):
+// rstd is common to the row, so
+//     amax|y| = rstd amax|h w|   and   q = (h w) (448 / amax|h w|),
+// and the sum of squares and the largest |h w| are gathered in the same pass over the
+// row: one exchange between the waves per row, and with block scales none at all
+// before the codes are stored (a block is the 16 lanes x 8 columns of one load).  The
+// row stays in registers between the pass and the codes, so the call moves what it has
+// to: 2 bytes per element in (4 with a residual), 1 out (2 more for h, 2 more for Y).
+// It is bound by HBM.
+//
+// Backward.  Each team of threads walks rows team, team + parts, ...: one pass gathers
+// mean(w dY xhat), the row (still in registers) gives dX, and every thread keeps the
+// sum of dY xhat of its own columns in fp32 over all its rows.  The teams' sums go to
+// the workspace and a second kernel adds them in a fixed order.
+#include "fp8gg_layer_internal.h"
+
+namespace fp8gg {
+
+namespace {
+
+__device__ __forceinline__ F8 load_weight(const void* w, int f32, int64_t j) {
+  F8 r;
+  if (f32) {
+    const f32x4 a = reinterpret_cast<const f32x4*>(w)[2 * j];
+    const f32x4 b = reinterpret_cast<const f32x4*>(w)[2 * j + 1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.v[i] = a[i];
+      r.v[4 + i] = b[i];
+    }
+  } else {
+    r = unpack_bf16(reinterpret_cast<const u32x4*>(w)[j]);
+  }
+  return r;
+}
+
+// A team of TPR threads works on one row; teams of one wave share a workgroup.
+constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+// Sum and maximum over the team.  `slot` alternates from row to row, so that one
+// barrier per row is enough: a slot is rewritten only after the next row's barrier,
+// which every thread reaches after it has read this row's values.
+template <int TPR>
+__device__ __forceinline__ void team_reduce(float& sum, uint32_t& most, int slot) {
+  sum = wave_reduce(sum, AddF());
+  most = wave_reduce(most, MaxU());
+  if constexpr (TPR > 64) {
+    __shared__ float sums[2][TPR / 64];
+    __shared__ uint32_t mosts[2][TPR / 64];
+    if ((threadIdx.x & 63) == 0) {
+      sums[slot][threadIdx.x >> 6] = sum;
+      mosts[slot][threadIdx.x >> 6] = most;
+    }
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < TPR / 64; ++w) {
+      sum += sums[slot][w];
+      most = umax(most, mosts[slot][w]);
+    }
+  }
+}
+
+template <int TPR, int NV, bool BLOCKED>
+__global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_quantize_kernel(NormArgs a) {
+  constexpr int kTeams = threads_of(TPR) / TPR;
+  const int lane = threadIdx.x % TPR;
+  const int team = threadIdx.x / TPR;
+  const int nvec = a.K / 8;
+  const float inv_k = 1.0f / (float)a.K;
+  int slot = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kTeams + team; row < a.rows; row += (int64_t)gridDim.x * kTeams) {
+    const int64_t base = row * nvec;
+    u32x4 raw[NV], res[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = i * TPR + lane;
+      raw[i] = res[i] = u32x4{0, 0, 0, 0};
+      if (j < nvec) {
+        raw[i] = reinterpret_cast<const u32x4*>(a.X)[base + j];
+        if (a.residual) res[i] = reinterpret_cast<const u32x4*>(a.residual)[base + j];
+      }
+    }
+    F8 hw[NV];
+    float sum = 0.f;
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = i * TPR + lane;
+      F8 h = unpack_bf16(raw[i]);
+      if (a.residual) {
+        const F8 r = unpack_bf16(res[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h.v[e] += r.v[e];
+        const u32x4 rounded = pack_bf16(h);
+        if (j < nvec) reinterpret_cast<u32x4*>(a.residual_out)[base + j] = rounded;
+        h = unpack_bf16(rounded);
+      }
+      F8 w{};
+      if (j < nvec) w = load_weight(a.weight, a.w_f32, j);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum = __builtin_fmaf(h.v[e], h.v[e], sum);
+        hw[i].v[e] = h.v[e] * w.v[e];
+      }
+      if constexpr (!BLOCKED) most = mag_max(hw[i], most);
+    }
+    float block_amax[NV];
+    if constexpr (BLOCKED) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int j = i * TPR + lane;
+        block_amax[i] = __uint_as_float(row16_reduce(mag_max(hw[i], 0), MaxU()));
+        if (j < nvec) reinterpret_cast<u32x2*>(a.XQ)[base + j] = codes_of(hw[i], inverse_scale(block_amax[i]));
+      }
+    }
+    team_reduce<TPR>(sum, most, slot);
+    slot ^= 1;
+    const float rstd = 1.0f / sqrtf(__builtin_fmaf(sum, inv_k, a.eps));
+    if constexpr (BLOCKED) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int j = i * TPR + lane;
+        if (j < nvec && (lane & 15) == 0)
+          a.x_scale[row * (nvec / 16) + j / 16] = block_amax[i] == 0.f ? 1.f : rstd * scale_of(block_amax[i]);
+      }
+    } else {
+      const float amax = __uint_as_float(most);
+      const float inv = inverse_scale(amax);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int j = i * TPR + lane;
+        if (j < nvec) reinterpret_cast<u32x2*>(a.XQ)[base + j] = codes_of(hw[i], inv);
+      }
+      if (lane == 0) a.x_scale[row] = amax == 0.f ? 1.f : rstd * scale_of(amax);
+    }
+    if (a.Y) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int j = i * TPR + lane;
+        F8 y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y.v[e] = hw[i].v[e] * rstd;
+        if (j < nvec) reinterpret_cast<u32x4*>(a.Y)[base + j] = pack_bf16(y);
+      }
+    }
+    if (a.rstd && lane == 0) a.rstd[row] = rstd;
+  }
+}
+
+template <int TPR, int NV>
+__global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_backward_kernel(NormBackwardArgs a) {
+  constexpr int kTeams = threads_of(TPR) / TPR;
+  const int lane = threadIdx.x % TPR;
+  const int team = blockIdx.x * kTeams + threadIdx.x / TPR;
+  if (team >= a.parts) return;   // whole waves; teams of several waves fill their workgroup
+  const int nvec = a.K / 8;
+  const float inv_k = 1.0f / (float)a.K;
+  F8 dw[NV] = {};
+  int slot = 0;
+  for (int64_t row = team; row < a.rows; row += a.parts) {
+    const int64_t base = row * nvec;
+    const float rstd = a.rstd[row];
+    u32x4 rdy[NV], rh[NV], rres[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = i * TPR + lane;
+      rdy[i] = rh[i] = rres[i] = u32x4{0, 0, 0, 0};
+      if (j < nvec) {
+        rdy[i] = reinterpret_cast<const u32x4*>(a.dY)[base + j];
+        rh[i] = reinterpret_cast<const u32x4*>(a.H)[base + j];
+        if (a.dresidual) rres[i] = reinterpret_cast<const u32x4*>(a.dresidual)[base + j];
+      }
+    }
+    float dot = 0.f;
+    F8 wdy[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = i * TPR + lane;
+      const F8 dy = unpack_bf16(rdy[i]), h = unpack_bf16(rh[i]);
+      F8 w{};
+      if (j < nvec) w = load_weight(a.weight, a.w_f32, j);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xhat = h.v[e] * rstd;
+        wdy[i].v[e] = w.v[e] * dy.v[e];
+        dot = __builtin_fmaf(wdy[i].v[e], xhat, dot);
+        dw[i].v[e] = __builtin_fmaf(dy.v[e], xhat, dw[i].v[e]);
+      }
+    }
+    uint32_t unused = 0;
+    team_reduce<TPR>(dot, unused, slot);
+    slot ^= 1;
+    const float c = dot * inv_k * rstd;   // times h: xhat * mean(w dY xhat)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = i * TPR + lane;
+      const F8 h = unpack_bf16(rh[i]), dr = unpack_bf16(rres[i]);
+      F8 dx;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        dx.v[e] = __builtin_fmaf(__builtin_fmaf(-h.v[e], c, wdy[i].v[e]), rstd, dr.v[e]);
+      if (j < nvec) reinterpret_cast<u32x4*>(a.dX)[base + j] = pack_bf16(dx);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = i * TPR + lane;
+    if (j < nvec) {
+      f32x4* p = reinterpret_cast<f32x4*>(a.partial + (int64_t)team * a.K) + 2 * j;
+      p[0] = f32x4{dw[i].v[0], dw[i].v[1], dw[i].v[2], dw[i].v[3]};
+      p[1] = f32x4{dw[i].v[4], dw[i].v[5], dw[i].v[6], dw[i].v[7]};
+    }
+  }
+}
+
+// dweight[k] = sum over the parts, in a fixed order: 16 lanes cover 64 columns, the
+// workgroup's 16 rows of lanes take every 16th part, then join through LDS.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float* partial, float* dweight, int K, int parts) {
+  __shared__ f32x4 joined[16][16];
+  const int col = blockIdx.x * 16 + (threadIdx.x & 15);
+  const int r = threadIdx.x >> 4;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (col < K / 4)
+    for (int p = r; p < parts; p += 16) s += reinterpret_cast<const f32x4*>(partial + (int64_t)p * K)[col];
+  joined[r][threadIdx.x & 15] = s;
+  __syncthreads();
+  if (r == 0 && col < K / 4) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += joined[i][threadIdx.x];
+    reinterpret_cast<f32x4*>(dweight)[col] = s;
+  }
+}
+
+template <int TPR, int NV>
+hipError_t launch_norm(const NormArgs& a, int block, hipStream_t stream) {
+  constexpr int kTeams = threads_of(TPR) / TPR;
+  const int64_t want = (a.rows + kTeams - 1) / kTeams;
+  const dim3 grid((uint32_t)(want < 65536 ? want : 65536)), threads(threads_of(TPR));
+  if (block)
+    hipLaunchKernelGGL((rmsnorm_quantize_kernel<TPR, NV, true>), grid, threads, 0, stream, a);
+  else
+    hipLaunchKernelGGL((rmsnorm_quantize_kernel<TPR, NV, false>), grid, threads, 0, stream, a);
+  return hipGetLastError();
+}
+
+template <int TPR, int NV>
+hipError_t launch_back(const NormBackwardArgs& a, hipStream_t stream) {
+  constexpr int kTeams = threads_of(TPR) / TPR;
+  hipLaunchKernelGGL((rmsnorm_backward_kernel<TPR, NV>), dim3((a.parts + kTeams - 1) / kTeams),
+                     dim3(threads_of(TPR)), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm_quantize(const NormArgs& a, int block, hipStream_t stream) {
+  if (a.rows == 0) return hipSuccess;
+  const int nvec = a.K / 8;
+  if (nvec <= 64) return launch_norm<64, 1>(a, block, stream);
+  if (nvec <= 256) return launch_norm<256, 1>(a, block, stream);
+  if (nvec <= 512) return launch_norm<256, 2>(a, block, stream);
+  if (nvec <= 1024) return launch_norm<256, 4>(a, block, stream);
+  return launch_norm<1024, 4>(a, block, stream);
+}
+
+int norm_backward_parts(int64_t rows, int64_t K) {
+  (void)K;
+  return (int)(rows < 512 ? rows : 512);
+}
+
+hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream) {
+  const int nvec = a.K / 8;
+  hipError_t e = hipSuccess;
+  if (a.rows > 0) {
+    if (nvec <= 64) e = launch_back<64, 1>(a, stream);
+    else if (nvec <= 256) e = launch_back<256, 1>(a, stream);
+    else if (nvec <= 512) e = launch_back<256, 2>(a, stream);
+    else if (nvec <= 1024) e = launch_back<256, 4>(a, stream);
+    else e = launch_back<1024, 4>(a, stream);
+  }
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(sum_parts_kernel, dim3((a.K / 4 + 15) / 16), dim3(256), 0, stream, a.partial, a.dweight, a.K,
+                     a.parts);
+  return hipGetLastError();
+}
+
+}  // namespace fp8gg
