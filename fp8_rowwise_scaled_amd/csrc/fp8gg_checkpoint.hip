@@ -125,29 +125,28 @@ __global__ void __launch_bounds__(256) silu_mul_backward_kernel(SiluBackwardArgs
 // ---------------------------------------------------------------------------
 //
 // Rows are cut into chunks of at most 128 rows of one group.  The first kernel writes
-// each chunk's largest magnitude per column; the second one joins the chunks of the
-// group, requantises its own 128 rows x 128 columns and turns them through LDS, so that
-// both sides are accessed in runs of at least 128 bytes.  The rows are read twice; the
-// second time the Infinity Cache holds them unless they pass 256 MB.
+// each chunk's largest magnitude per column, and where the chunk lies; the second one
+// joins the chunks of the group, requantises its own 128 rows x 128 columns and turns
+// them through LDS, so that both sides are accessed in runs of at least 128 bytes.  The
+// rows are read twice; the second time the Infinity Cache holds them unless they pass
+// 256 MB.
 
 constexpr int kTile = 128;             // columns of the second kernel's tile
 constexpr int kLdsStride = 33;         // words per column: 128 codes and one of padding
 
-struct Chunk {
-  int group;         // -1: past the last chunk
-  int rows;          // rows of the chunk
-  int first;         // first chunk of its group
-  int chunks;        // chunks of its group
-  int64_t row;       // first row in X
-  int64_t col;       // first column in XT
-  int64_t last;      // one past the group's last column (a multiple of 16)
+// 64 groups, one per lane: counts clamped as in the stacked layout (negative ones to 0,
+// ends to R), and where each group's rows, columns and chunks end.
+struct GroupSpan {
+  int64_t begin, end;                  // rows
+  int64_t cols, cols_end;              // columns, a multiple of 16, and their end
+  int chunks, chunks_end;
 };
 
-// Finds chunk c; every wave of the workgroup does so by itself.  Counts are clamped as
-// in the stacked layout: negative ones to 0, ends to R.
-__device__ __forceinline__ Chunk find_chunk(const KOffsetsArgs& a, int c) {
+// Calls visit(first group, the lane's span) for every 64 groups until it returns true;
+// all lanes of the wave take part.  Returns the end of the last group's columns.
+template <typename Visit>
+__device__ __forceinline__ int64_t scan_groups(const KOffsetsArgs& a, Visit visit) {
   const int lane = threadIdx.x & 63;
-  Chunk f{-1, 0, 0, 0, 0, 0, 0};
   int64_t rows_before = 0, cols_before = 0;
   int chunks_before = 0;
   for (int g0 = 0; g0 < a.G; g0 += 64) {
@@ -158,43 +157,47 @@ __device__ __forceinline__ Chunk find_chunk(const KOffsetsArgs& a, int c) {
       const int64_t y = __shfl_up(end, off, 64);
       if (lane >= off) end += y;
     }
-    end += rows_before;
-    int64_t begin = end - m;
-    begin = begin > a.R ? a.R : begin;
-    end = end > a.R ? a.R : end;
-    const int64_t size = end - begin;
-    const int n = (int)((size + kChunkRows - 1) / kChunkRows);
-    const int64_t cols = (size + 15) / 16 * 16;
-    int n_end = n;
-    int64_t cols_end = cols;
+    GroupSpan s;
+    s.end = end + rows_before;
+    s.begin = s.end - m;
+    s.begin = s.begin > a.R ? a.R : s.begin;
+    s.end = s.end > a.R ? a.R : s.end;
+    const int64_t size = s.end - s.begin;
+    s.chunks = s.chunks_end = (int)((size + kChunkRows - 1) / kChunkRows);
+    s.cols = s.cols_end = (size + 15) / 16 * 16;
     for (int off = 1; off < 64; off <<= 1) {
-      const int y = __shfl_up(n_end, off, 64);
-      const int64_t z = __shfl_up(cols_end, off, 64);
+      const int y = __shfl_up(s.chunks_end, off, 64);
+      const int64_t z = __shfl_up(s.cols_end, off, 64);
       if (lane >= off) {
-        n_end += y;
-        cols_end += z;
+        s.chunks_end += y;
+        s.cols_end += z;
       }
     }
-    n_end += chunks_before;
-    cols_end += cols_before;
-    const uint64_t hit = __ballot(c >= n_end - n && c < n_end);
-    if (hit) {
-      const int src = __ffsll((unsigned long long)hit) - 1;
-      f.group = g0 + src;
-      f.chunks = __shfl(n, src, 64);
-      f.first = __shfl(n_end, src, 64) - f.chunks;
-      const int64_t begins = __shfl(begin, src, 64), ends = __shfl(end, src, 64);
-      f.last = __shfl(cols_end, src, 64);
-      f.row = begins + (int64_t)(c - f.first) * kChunkRows;
-      f.rows = (int)(ends - f.row < kChunkRows ? ends - f.row : kChunkRows);
-      f.col = f.last - __shfl(cols, src, 64) + (int64_t)(c - f.first) * kChunkRows;
-      return f;
-    }
-    rows_before = __shfl(end, 63, 64);
-    chunks_before = __shfl(n_end, 63, 64);
-    cols_before = __shfl(cols_end, 63, 64);
+    s.chunks_end += chunks_before;
+    s.cols_end += cols_before;
+    if (visit(g0, s)) break;
+    rows_before = __shfl(s.end, 63, 64);
+    chunks_before = __shfl(s.chunks_end, 63, 64);
+    cols_before = __shfl(s.cols_end, 63, 64);
   }
-  f.last = cols_before;
+  return cols_before;
+}
+
+__device__ __forceinline__ KChunk find_chunk(const KOffsetsArgs& a, int c) {
+  KChunk f{0, 0, -1, 0, 0, 0};
+  scan_groups(a, [&](int g0, const GroupSpan& s) {
+    const uint64_t hit = __ballot(c >= s.chunks_end - s.chunks && c < s.chunks_end);
+    if (!hit) return false;
+    const int src = __ffsll((unsigned long long)hit) - 1;
+    f.group = g0 + src;
+    f.chunks = __shfl(s.chunks, src, 64);
+    f.first = __shfl(s.chunks_end, src, 64) - f.chunks;
+    f.row = __shfl(s.begin, src, 64) + (int64_t)(c - f.first) * kChunkRows;
+    const int64_t left = __shfl(s.end, src, 64) - f.row;
+    f.rows = (int)(left < kChunkRows ? left : kChunkRows);
+    f.col = __shfl(s.cols_end, src, 64) - __shfl(s.cols, src, 64) + (int64_t)(c - f.first) * kChunkRows;
+    return true;
+  });
   return f;
 }
 
@@ -225,17 +228,23 @@ __global__ void __launch_bounds__(256) column_amax_kernel(KOffsetsArgs a, int ti
   constexpr int kLanes = 512 / W, kRows = 256 / kLanes;
   __shared__ uint32_t most[kRows][512 + 4];
   const int chunk = blockIdx.x / tiles, col0 = (int)(blockIdx.x % tiles) * 512;
-  const Chunk f = find_chunk(a, chunk);
+  const KChunk f = find_chunk(a, chunk);
+  if (col0 == 0 && threadIdx.x == 0) a.table[chunk] = f;
   if (f.group < 0) return;
   const int lx = threadIdx.x % kLanes, ly = threadIdx.x / kLanes;
   const int col = col0 + lx * W;
   uint32_t m[W] = {};
   if (col < a.K) {
-    for (int r = ly; r < f.rows; r += kRows) {
-      float v[W];
-      load_values<E4M3>(a, f.row + r, col, v);
+    // four rows in flight
+    for (int r = ly; r < f.rows; r += 4 * kRows) {
+      float v[4][W] = {};
 #pragma unroll
-      for (int e = 0; e < W; ++e) m[e] = umax(m[e], mag(v[e]));
+      for (int i = 0; i < 4; ++i)
+        if (r + i * kRows < f.rows) load_values<E4M3>(a, f.row + r + i * kRows, col, v[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < W; ++e) m[e] = umax(m[e], mag(v[i][e]));
     }
   }
 #pragma unroll
@@ -260,25 +269,24 @@ __global__ void __launch_bounds__(256) transpose_quantize_kernel(KOffsetsArgs a,
   __shared__ float inverse[kTile];
   const int chunk = blockIdx.x / tiles, col0 = (int)(blockIdx.x % tiles) * kTile;
   if (chunk == chunks) {
-    const Chunk f = find_chunk(a, 0x7FFFFFFF);
-    const int64_t tail = (a.cap - f.last) / 16;
+    const int64_t used = scan_groups(a, [&](int g0, const GroupSpan& s) {
+      if (threadIdx.x >= 64) return false;
+      const int lane = threadIdx.x;
+      if (col0 == 0 && g0 + lane < a.G) a.k_offsets[g0 + lane] = (int32_t)s.cols_end;
+      for (uint64_t empty = __ballot(g0 + lane < a.G && s.chunks == 0); empty; empty &= empty - 1) {
+        float* scales = a.t_scale + (int64_t)(g0 + __ffsll((unsigned long long)empty) - 1) * a.K;
+        for (int k = col0 + lane; k < col0 + kTile && k < a.K; k += 64) scales[k] = 1.f;
+      }
+      return false;
+    });
+    const int64_t tail = (a.cap - used) / 16;
     for (int64_t i = threadIdx.x; i < tail * kTile; i += 256) {
       const int k = col0 + (int)(i / tail);
-      if (k < a.K) *reinterpret_cast<u32x4*>(a.XT + k * a.cap + f.last + (i % tail) * 16) = u32x4{0, 0, 0, 0};
-    }
-    int64_t row = 0, col = 0;
-    for (int g = 0; g < a.G; ++g) {
-      int64_t m = a.M_sizes[g];
-      m = m < 0 ? 0 : (m > a.R - row ? a.R - row : m);
-      row += m;
-      col += (m + 15) / 16 * 16;
-      if (m == 0 && (int)threadIdx.x < kTile && col0 + (int)threadIdx.x < a.K)
-        a.t_scale[(int64_t)g * a.K + col0 + threadIdx.x] = 1.f;
-      if (col0 == 0 && threadIdx.x == 0) a.k_offsets[g] = (int32_t)col;
+      if (k < a.K) *reinterpret_cast<u32x4*>(a.XT + k * a.cap + used + (i % tail) * 16) = u32x4{0, 0, 0, 0};
     }
     return;
   }
-  const Chunk f = find_chunk(a, chunk);
+  const KChunk f = a.table[chunk];
   if (f.group < 0) return;
   if (threadIdx.x < kTile) {
     const int k = col0 + threadIdx.x;

@@ -2,9 +2,11 @@
 // the weighted combine, and its gradients.
 //
 // All three are driven from the token side: dst_row[t, j] is the place of token t's
-// j-th row in the experts' order, the same for every lane of a workgroup, so places and
-// weights are scalar loads and each token's own row is read (or written) once.  They
-// move every byte once and are bound by HBM.
+// j-th row in the experts' order, the same for every lane of a workgroup.  Lane j of
+// each wave loads place (and weight) j, all of them in one load, and the loop over j
+// reads them from that lane; loading them one by one in the loop waits for memory k
+// times over.  Each token's own row is read (or written) once: every byte moves once,
+// and the calls are bound by HBM.
 #include "fp8gg_layer_internal.h"
 
 namespace fp8gg {
@@ -15,7 +17,25 @@ constexpr int kThreads = 256;
 constexpr int kMaxPlaces = 64;
 constexpr int64_t kMaxGrid = 1 << 20;
 
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// Places and weights of one token, the j-th in lane j (k <= 64).  Read with every lane
+// of the wave active.
+struct Places {
+  int row;
+  float weight;
+};
+__device__ __forceinline__ Places load_places(const int32_t* dst_row, const float* weights, int64_t t, int k) {
+  const int lane = threadIdx.x & 63;
+  Places p{-1, 1.f};
+  if (lane < k) {
+    p.row = dst_row[t * k + lane];
+    if (weights) p.weight = weights[t * k + lane];
+  }
+  return p;
+}
+__device__ __forceinline__ int64_t row_of(const Places& p, int j) { return __builtin_amdgcn_readlane(p.row, j); }
+__device__ __forceinline__ float weight_of(const Places& p, int j) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p.weight), j));
+}
 
 // One workgroup copies 4 KiB of one token's codes (16 bytes per thread) to its k places.
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(DispatchArgs a, int chunks, int64_t work) {
@@ -26,8 +46,9 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(DispatchArgs a, int 
     const int v = c * kThreads + threadIdx.x;
     u32x4 x = {0, 0, 0, 0};
     if (v < nvec) x = reinterpret_cast<const u32x4*>(a.XQ)[t * nvec + v];
+    const Places p = load_places(a.dst_row, nullptr, t, a.k);
     for (int j = 0; j < a.k; ++j) {
-      const int64_t r = uniform(a.dst_row[t * a.k + j]);
+      const int64_t r = row_of(p, j);
       if (r < 0 || r >= a.R) continue;
       if (v < nvec) reinterpret_cast<u32x4*>(a.XQs)[r * nvec + v] = x;
       if (c == 0)
@@ -43,7 +64,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(ExchangeArgs a, int c
   for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
     const int64_t t = i / chunks;
     const int v = (int)(i - t * chunks) * kThreads + threadIdx.x;
-    if (v >= nvec) continue;
+    const bool inside = v < nvec;
+    const Places p = load_places(a.dst_row, a.weights, t, a.k);
     F8 sum = {};
     // up to eight rows in flight
     for (int j0 = 0; j0 < a.k; j0 += 8) {
@@ -54,10 +76,10 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(ExchangeArgs a, int c
         y[u] = u32x4{0, 0, 0, 0};
         w[u] = 0.f;
         if (j0 + u < a.k) {
-          const int64_t r = uniform(a.dst_row[t * a.k + j0 + u]);
+          const int64_t r = row_of(p, j0 + u);
           if (r >= 0 && r < a.R) {
-            y[u] = reinterpret_cast<const u32x4*>(a.rows_in)[r * nvec + v];
-            w[u] = a.weights ? a.weights[t * a.k + j0 + u] : 1.f;
+            w[u] = weight_of(p, j0 + u);
+            if (inside) y[u] = reinterpret_cast<const u32x4*>(a.rows_in)[r * nvec + v];
           }
         }
       }
@@ -68,6 +90,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(ExchangeArgs a, int c
         for (int e = 0; e < 8; ++e) sum.v[e] = __builtin_fmaf(w[u], f.v[e], sum.v[e]);
       }
     }
+    if (!inside) continue;
     if (a.other) {
       const F8 f = unpack_bf16(reinterpret_cast<const u32x4*>(a.other)[t * nvec + v]);
 #pragma unroll
@@ -96,11 +119,12 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(ExchangeArgs
         if (v < nvec) d[i] = reinterpret_cast<const u32x4*>(a.rows_in)[t * nvec + v];
       }
     }
+    const Places p = load_places(a.dst_row, a.weights, t, a.k);
     for (int j = 0; j < a.k; ++j) {
-      const int64_t r = uniform(a.dst_row[t * a.k + j]);
+      const int64_t r = row_of(p, j);
       float dot = 0.f;
       if (r >= 0 && r < a.R) {
-        const float w = a.weights ? a.weights[t * a.k + j] : 1.f;
+        const float w = weight_of(p, j);
         const auto one = [&](const u32x4& raw, int v) {
           const F8 g = unpack_bf16(raw);
           if (dots) {

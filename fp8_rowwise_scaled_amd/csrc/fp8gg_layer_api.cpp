@@ -346,7 +346,7 @@ int64_t f8f8bf16_k_offsets_capacity(int64_t R, int64_t G) {
 
 int64_t f8f8bf16_quantize_k_offsets_workspace(int64_t R, int64_t G, int64_t K) {
   if (R <= 0 || G <= 0 || K <= 0 || R > kMaxDim || K > kMaxDim || G > 1024) return 0;
-  return fp8gg::k_offsets_chunks(R, G) * K * 4;
+  return fp8gg::k_offsets_chunks(R, G) * (K * 4 + (int64_t)sizeof(fp8gg::KChunk));
 }
 
 fp8gg_status f8f8bf16_quantize_k_offsets(const void* X, int x_dtype, const float* x_scale, int64_t scale_cols,
@@ -375,8 +375,10 @@ fp8gg_status f8f8bf16_quantize_k_offsets(const void* X, int x_dtype, const float
                    {"t_scale", t_scale, 4 * G * K, 4, true, false},
                    {"k_offsets", k_offsets, 4 * G, 4, true, false},
                    {"workspace", workspace, need, 16, true, true}}));
-  const fp8gg::KOffsetsArgs a{X, x_scale, M_sizes, XT, t_scale, k_offsets, static_cast<float*>(workspace), R, cap,
-                              (int32_t)G, (int32_t)K, (int32_t)scale_cols};
+  float* partial = static_cast<float*>(workspace);   // K % 16 == 0 keeps the table behind it aligned
+  const fp8gg::KOffsetsArgs a{X, x_scale, M_sizes, XT, t_scale, k_offsets, partial,
+                              reinterpret_cast<fp8gg::KChunk*>(partial + chunks * K), R, cap, (int32_t)G, (int32_t)K,
+                              (int32_t)scale_cols};
   return launched(fp8gg::launch_quantize_k_offsets(a, static_cast<hipStream_t>(stream)), "quantize_k_offsets");
 }
 

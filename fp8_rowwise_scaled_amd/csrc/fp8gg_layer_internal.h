@@ -105,6 +105,16 @@ struct SiluBackwardArgs {
   int32_t I;
 };
 
+// At most kChunkRows rows of one group.
+struct KChunk {
+  int64_t row;       // first row in X
+  int64_t col;       // first column in XT
+  int32_t group;     // -1: past the last chunk
+  int32_t rows;
+  int32_t first;     // the group's first chunk
+  int32_t chunks;    // the group's chunks
+};
+
 struct KOffsetsArgs {
   const void* X;                // bf16, or e4m3fn codes when x_scale is given
   const float* x_scale;
@@ -112,7 +122,8 @@ struct KOffsetsArgs {
   uint8_t* XT;
   float* t_scale;
   int32_t* k_offsets;
-  float* partial;               // [row chunks, K] largest magnitudes
+  float* partial;               // [chunks, K] largest magnitudes
+  KChunk* table;                // [chunks]
   int64_t R, cap;
   int32_t G, K, scale_cols;
 };

@@ -217,20 +217,25 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_backward_kernel(NormB
   }
 }
 
-// dweight[k] = sum over the parts, in a fixed order: 16 lanes cover 64 columns, the
-// workgroup's 16 rows of lanes take every 16th part, then join through LDS.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float* partial, float* dweight, int K, int parts) {
-  __shared__ f32x4 joined[16][16];
-  const int col = blockIdx.x * 16 + (threadIdx.x & 15);
-  const int r = threadIdx.x >> 4;
+// dweight[k] = sum over the parts, in a fixed order: 8 lanes cover 32 columns, the
+// workgroup's 32 rows of lanes take every 32nd part (eight loads in flight), then join
+// through LDS.
+constexpr int kSumCols = 32;
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ partial, float* __restrict__ dweight,
+                                                        int K, int parts) {
+  __shared__ f32x4 joined[32][kSumCols / 4];
+  const int lane = threadIdx.x % (kSumCols / 4), r = threadIdx.x / (kSumCols / 4);
+  const int col = blockIdx.x * (kSumCols / 4) + lane;
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  if (col < K / 4)
-    for (int p = r; p < parts; p += 16) s += reinterpret_cast<const f32x4*>(partial + (int64_t)p * K)[col];
-  joined[r][threadIdx.x & 15] = s;
+  if (col < K / 4) {
+#pragma unroll 8
+    for (int p = r; p < parts; p += 32) s += reinterpret_cast<const f32x4*>(partial + (int64_t)p * K)[col];
+  }
+  joined[r][lane] = s;
   __syncthreads();
   if (r == 0 && col < K / 4) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += joined[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) s += joined[i][lane];
     reinterpret_cast<f32x4*>(dweight)[col] = s;
   }
 }
@@ -283,8 +288,8 @@ hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream
     else e = launch_back<1024, 4>(a, stream);
   }
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(sum_parts_kernel, dim3((a.K / 4 + 15) / 16), dim3(256), 0, stream, a.partial, a.dweight, a.K,
-                     a.parts);
+  hipLaunchKernelGGL(sum_parts_kernel, dim3((a.K + kSumCols - 1) / kSumCols), dim3(256), 0, stream, a.partial,
+                     a.dweight, a.K, a.parts);
   return hipGetLastError();
 }
 
