@@ -135,86 +135,101 @@ constexpr int kTile = 128;             // columns of the second kernel's tile
 constexpr int kLdsStride = 33;         // words per column: 128 codes and one of padding
 
 // 64 groups, one per lane: counts clamped as in the stacked layout (negative ones to 0,
-// ends to R), and where each group's rows, columns and chunks end.
+// ends to R), and where each group's rows, columns and chunks end.  R, and with it every
+// number here, is below 2^31.
 struct GroupSpan {
-  int64_t begin, end;                  // rows
-  int64_t cols, cols_end;              // columns, a multiple of 16, and their end
-  int chunks, chunks_end;
+  uint32_t begin, end;                 // rows
+  uint32_t cols, cols_end;             // columns, a multiple of 16, and their end
+  uint32_t chunks, chunks_end;
+};
+
+// Sums that stop at R: ends cut at R add up in any order.
+struct AddUpTo {
+  uint32_t most;
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return umin(a + b, most); }
 };
 
 // Calls visit(first group, the lane's span) for every 64 groups until it returns true;
 // all lanes of the wave take part.  Returns the end of the last group's columns.
 template <typename Visit>
-__device__ __forceinline__ int64_t scan_groups(const KOffsetsArgs& a, Visit visit) {
+__device__ __forceinline__ uint32_t scan_groups(const KOffsetsArgs& a, Visit visit) {
   const int lane = threadIdx.x & 63;
-  int64_t rows_before = 0, cols_before = 0;
-  int chunks_before = 0;
+  const AddUpTo add{(uint32_t)a.R};
+  uint32_t rows_before = 0, cols_before = 0, chunks_before = 0;
   for (int g0 = 0; g0 < a.G; g0 += 64) {
     int64_t m = g0 + lane < a.G ? a.M_sizes[g0 + lane] : 0;
     m = m < 0 ? 0 : (m > a.R ? a.R : m);
-    int64_t end = m;
-    for (int off = 1; off < 64; off <<= 1) {
-      const int64_t y = __shfl_up(end, off, 64);
-      if (lane >= off) end += y;
-    }
+    const uint32_t sum = wave_scan((uint32_t)m, add);
     GroupSpan s;
-    s.end = end + rows_before;
-    s.begin = s.end - m;
-    s.begin = s.begin > a.R ? a.R : s.begin;
-    s.end = s.end > a.R ? a.R : s.end;
-    const int64_t size = s.end - s.begin;
-    s.chunks = s.chunks_end = (int)((size + kChunkRows - 1) / kChunkRows);
-    s.cols = s.cols_end = (size + 15) / 16 * 16;
-    for (int off = 1; off < 64; off <<= 1) {
-      const int y = __shfl_up(s.chunks_end, off, 64);
-      const int64_t z = __shfl_up(s.cols_end, off, 64);
-      if (lane >= off) {
-        s.chunks_end += y;
-        s.cols_end += z;
-      }
-    }
-    s.chunks_end += chunks_before;
-    s.cols_end += cols_before;
+    s.end = add(rows_before, sum);
+    // the group before this one ends where this one begins (lane 0: the last one of the 64 before)
+    const uint32_t prior = (uint32_t)__shfl_up((int)s.end, 1, 64);
+    s.begin = lane == 0 ? rows_before : prior;
+    const uint32_t size = s.end - s.begin;
+    s.chunks = (size + kChunkRows - 1) / kChunkRows;
+    s.cols = (size + 15) / 16 * 16;
+    s.chunks_end = chunks_before + wave_scan(s.chunks, AddF());
+    s.cols_end = cols_before + wave_scan(s.cols, AddF());
     if (visit(g0, s)) break;
-    rows_before = __shfl(s.end, 63, 64);
-    chunks_before = __shfl(s.chunks_end, 63, 64);
-    cols_before = __shfl(s.cols_end, 63, 64);
+    rows_before = (uint32_t)__builtin_amdgcn_readlane((int)s.end, 63);
+    chunks_before = (uint32_t)__builtin_amdgcn_readlane((int)s.chunks_end, 63);
+    cols_before = (uint32_t)__builtin_amdgcn_readlane((int)s.cols_end, 63);
   }
   return cols_before;
 }
 
-__device__ __forceinline__ KChunk find_chunk(const KOffsetsArgs& a, int c) {
+__device__ __forceinline__ int from_lane(uint32_t x, int lane) { return __builtin_amdgcn_readlane((int)x, lane); }
+
+__device__ __forceinline__ KChunk find_chunk(const KOffsetsArgs& a, uint32_t c) {
   KChunk f{0, 0, -1, 0, 0, 0};
   scan_groups(a, [&](int g0, const GroupSpan& s) {
     const uint64_t hit = __ballot(c >= s.chunks_end - s.chunks && c < s.chunks_end);
     if (!hit) return false;
-    const int src = __ffsll((unsigned long long)hit) - 1;
+    const int src = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
     f.group = g0 + src;
-    f.chunks = __shfl(s.chunks, src, 64);
-    f.first = __shfl(s.chunks_end, src, 64) - f.chunks;
-    f.row = __shfl(s.begin, src, 64) + (int64_t)(c - f.first) * kChunkRows;
-    const int64_t left = __shfl(s.end, src, 64) - f.row;
-    f.rows = (int)(left < kChunkRows ? left : kChunkRows);
-    f.col = __shfl(s.cols_end, src, 64) - __shfl(s.cols, src, 64) + (int64_t)(c - f.first) * kChunkRows;
+    f.chunks = from_lane(s.chunks, src);
+    f.first = from_lane(s.chunks_end, src) - f.chunks;
+    const int at = ((int)c - f.first) * kChunkRows;
+    f.row = from_lane(s.begin, src) + at;
+    const int left = from_lane(s.end, src) - f.row;
+    f.rows = left < kChunkRows ? left : kChunkRows;
+    f.col = from_lane(s.cols_end, src) - from_lane(s.cols, src) + at;
     return true;
   });
   return f;
 }
 
-// E4M3: 16 codes per thread and load, else 8 bf16 values.
+// One load of a row: 16 codes and their row's scale (E4M3), or 8 bf16 values.
 template <bool E4M3>
-__device__ __forceinline__ void load_values(const KOffsetsArgs& a, int64_t row, int col, float* v) {
+struct Raw {
+  u32x4 q;
+  float scale;
+};
+
+template <bool E4M3>
+__device__ __forceinline__ Raw<E4M3> load_raw(const KOffsetsArgs& a, int64_t row, int col) {
+  Raw<E4M3> r;
   if constexpr (E4M3) {
-    const u32x4 q = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(a.X) + row * a.K + col);
-    const float s = a.x_scale[row * a.scale_cols + (a.scale_cols > 1 ? col / 128 : 0)];
-    const F8 lo = values_of(u32x2{q[0], q[1]}), hi = values_of(u32x2{q[2], q[3]});
+    r.q = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(a.X) + row * a.K + col);
+    r.scale = a.x_scale[row * a.scale_cols + (a.scale_cols > 1 ? col / 128 : 0)];
+  } else {
+    r.q = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.X) + row * a.K + col);
+    r.scale = 1.f;
+  }
+  return r;
+}
+
+template <bool E4M3>
+__device__ __forceinline__ void values(const Raw<E4M3>& r, float (&v)[E4M3 ? 16 : 8]) {
+  if constexpr (E4M3) {
+    const F8 lo = values_of(u32x2{r.q[0], r.q[1]}), hi = values_of(u32x2{r.q[2], r.q[3]});
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      v[e] = lo.v[e] * s;
-      v[8 + e] = hi.v[e] * s;
+      v[e] = lo.v[e] * r.scale;
+      v[8 + e] = hi.v[e] * r.scale;
     }
   } else {
-    const F8 f = unpack_bf16(*reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.X) + row * a.K + col));
+    const F8 f = unpack_bf16(r.q);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = f.v[e];
   }
@@ -235,16 +250,21 @@ __global__ void __launch_bounds__(256) column_amax_kernel(KOffsetsArgs a, int ti
   const int col = col0 + lx * W;
   uint32_t m[W] = {};
   if (col < a.K) {
-    // four rows in flight
-    for (int r = ly; r < f.rows; r += 4 * kRows) {
-      float v[4][W] = {};
+    // eight rows in flight
+    for (int r = ly; r < f.rows; r += 8 * kRows) {
+      Raw<E4M3> raw[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (r + i * kRows < f.rows) load_values<E4M3>(a, f.row + r + i * kRows, col, v[i]);
+      for (int i = 0; i < 8; ++i) {
+        raw[i] = Raw<E4M3>{{0, 0, 0, 0}, 0.f};
+        if (r + i * kRows < f.rows) raw[i] = load_raw<E4M3>(a, f.row + r + i * kRows, col);
+      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 8; ++i) {
+        float v[W];
+        values<E4M3>(raw[i], v);
 #pragma unroll
-        for (int e = 0; e < W; ++e) m[e] = umax(m[e], mag(v[i][e]));
+        for (int e = 0; e < W; ++e) m[e] = umax(m[e], mag(v[e]));
+      }
     }
   }
 #pragma unroll
@@ -288,32 +308,45 @@ __global__ void __launch_bounds__(256) transpose_quantize_kernel(KOffsetsArgs a,
   }
   const KChunk f = a.table[chunk];
   if (f.group < 0) return;
+  const int lx = threadIdx.x % kLanes, ly = threadIdx.x / kLanes;
+  const int col = col0 + lx * W;
+  // four neighbouring rows per thread: their codes of one column are one LDS word.  The
+  // rows are asked for before the scales are put together.
+  constexpr int kPasses = kChunkRows / (kRowLanes * 4);
+  Raw<E4M3> raw[kPasses][4];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (p * kRowLanes + ly) * 4 + i;
+      raw[p][i] = Raw<E4M3>{{0, 0, 0, 0}, 0.f};
+      if (r < f.rows && col < a.K) raw[p][i] = load_raw<E4M3>(a, f.row + r, col);
+    }
   if (threadIdx.x < kTile) {
     const int k = col0 + threadIdx.x;
     uint32_t m = 0;
-    if (k < a.K)
+    if (k < a.K) {
+#pragma unroll 4
       for (int c = f.first; c < f.first + f.chunks; ++c) m = umax(m, __float_as_uint(a.partial[(int64_t)c * a.K + k]));
+    }
     const float amax = __uint_as_float(m);
     inverse[threadIdx.x] = inverse_scale(amax);
     if (k < a.K && chunk == f.first) a.t_scale[(int64_t)f.group * a.K + k] = scale_of(amax);
   }
   __syncthreads();
-  const int lx = threadIdx.x % kLanes, ly = threadIdx.x / kLanes;
-  const int col = col0 + lx * W;
   float inv[W];
 #pragma unroll
   for (int e = 0; e < W; ++e) inv[e] = inverse[lx * W + e];
-  // four neighbouring rows per thread: their codes of one column are one LDS word
-  for (int r = ly * 4; r < kChunkRows; r += kRowLanes * 4) {
-    float v[4][W] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (r + i < f.rows && col < a.K) load_values<E4M3>(a, f.row + r + i, col, v[i]);
+  for (int p = 0; p < kPasses; ++p) {
+    float v[4][W];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) values<E4M3>(raw[p][i], v[i]);
 #pragma unroll
     for (int e = 0; e < W; ++e) {
       int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[0][e] * inv[e], v[1][e] * inv[e], 0, false);
       q = __builtin_amdgcn_cvt_pk_fp8_f32(v[2][e] * inv[e], v[3][e] * inv[e], q, true);
-      turned[(lx * W + e) * kLdsStride + r / 4] = (uint32_t)q;
+      turned[(lx * W + e) * kLdsStride + p * kRowLanes + ly] = (uint32_t)q;
     }
   }
   __syncthreads();

@@ -238,7 +238,7 @@ fp8gg_status f8f8bf16_route(const void* logits, int logits_dtype, const float* b
   const fp8gg::RouteArgs a{logits, bias, weights, ids, M_sizes, dst_row, static_cast<int32_t*>(workspace), T,
                            (int32_t)E, (int32_t)k, (int32_t)n_group, (int32_t)topk_group, group_top,
                            logits_dtype == FP8GG_DTYPE_BF16, score == FP8GG_SCORE_SIGMOID, renormalize != 0,
-                           fp8gg::route_block_tokens(T), scale};
+                           fp8gg::route_block_tokens(T), scale, 0};
   return launched(fp8gg::launch_route(a, static_cast<hipStream_t>(stream)), "route");
 }
 

@@ -52,6 +52,7 @@ struct RouteArgs {
   int32_t bf16, sigmoid, renormalize;
   int32_t block_tokens;         // tokens of one workgroup (a multiple of 64)
   float scale;
+  int32_t token_lds;            // bytes of LDS per token (set by the launcher)
 };
 
 struct RouteBackwardArgs {
@@ -107,8 +108,8 @@ struct SiluBackwardArgs {
 
 // At most kChunkRows rows of one group.
 struct KChunk {
-  int64_t row;       // first row in X
-  int64_t col;       // first column in XT
+  int32_t row;       // first row in X
+  int32_t col;       // first column in XT
   int32_t group;     // -1: past the last chunk
   int32_t rows;
   int32_t first;     // the group's first chunk
@@ -292,6 +293,18 @@ __device__ __forceinline__ T swap_reduce(T x, Op op) {
 template <typename T, typename Op>
 __device__ __forceinline__ T wave_reduce(T x, Op op) {
   return swap_reduce<true>(swap_reduce<false>(row16_reduce(x, op), op), op);
+}
+
+// Inclusive scan over the wave: shifts within rows of 16 lanes, then the last lane of a
+// row (of the lower half) to the rows after it.  0 is op's neutral element.
+template <typename Op>
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x, Op op) {
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, false));   // row_shr 1
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, false));   // row_shr 2
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, false));   // row_shr 4
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, false));   // row_shr 8
+  x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false));   // row_bcast 15
+  return op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false));   // row_bcast 31
 }
 
 struct AddF {

@@ -2,17 +2,18 @@
 // its gradient (gfx950).
 //
 // Choice.  A team of 16 lanes (E <= 256; else the wave's 64) holds one token's keys in
-// registers, up to 16 per lane.  Each of the k rounds takes the largest key (a scan of
-// the lane's own, then moves inside the row of 16 lanes, no LDS) and, among equal ones,
-// the lowest index, and takes it out.
+// registers, up to 16 per lane.  The k-th largest of 16 lanes' own maxima bounds the
+// k-th largest key from below; the keys that reach it, a dozen or so of 256, go to LDS,
+// and each of them finds its rank by comparing itself with the others.  That is about a
+// third of the instructions of k rounds of a maximum over the team (48 us at 16384
+// tokens, 256 experts in 8 groups, k = 8).
 //
 // What has to be compared exactly.  Scores rise with their logits, so without a bias
 // and with groups ranked by their best expert the logits themselves are the keys: exact
 // and no exponential.  Otherwise keys are p + bias or sums of two of them in fp32, off
-// by a few units in the last place; every pair of neighbours in the order taken (and the
-// border between kept and dropped groups) is checked, and where two are nearer than the
-// error bound the token is decided again in fp64.  With scores spread like a router's
-// that is one token in a few hundred.
+// by a few units in the last place; where two of the ranked keys (or the last group kept
+// and the first one dropped) are nearer than the error bound, those keys are computed
+// again in fp64 and ranked by that.
 //
 // Plan.  A stable counting sort of the pairs by expert: each workgroup counts its
 // tokens' experts, the second kernel adds up the counts before its own block and ranks
@@ -41,14 +42,6 @@ __device__ __forceinline__ T team_reduce(T x, Op op) {
   else return wave_reduce(x, op);
 }
 
-// Whether any lane of the token's team says so.
-template <int L>
-__device__ __forceinline__ bool team_any(bool p, int tok) {
-  const uint64_t b = __ballot(p);
-  if constexpr (L == 64) return b != 0;
-  else return ((b >> (tok * L)) & ((uint64_t(1) << (L & 63)) - 1)) != 0;
-}
-
 // The expert of the lane's v-th key.  From four keys per lane on, four neighbouring
 // experts sit in one lane, so that a row is read with 16-byte (bf16: 8-byte) loads.
 // Expert numbers rise with v within a lane.
@@ -62,10 +55,9 @@ template <typename T>
 __device__ __forceinline__ T none() { return -__builtin_huge_valf(); }
 
 // A logit or bias as it counts: NaN and -infinity take the expert out, +infinity is the
-// largest finite value, -0 is 0.
+// largest finite value.
 __device__ __forceinline__ float counted(float x) {
-  const float y = x + 0.0f;
-  return !(y > -__builtin_huge_valf()) ? -__builtin_huge_valf() : (y > 3.402823466e38f ? 3.402823466e38f : y);
+  return __builtin_fminf(__builtin_fmaxf(x, -__builtin_huge_valf()), 3.402823466e38f);
 }
 
 __device__ __forceinline__ float logit_at(const void* logits, int bf16, int64_t i) {
@@ -104,53 +96,41 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int l, f
   }
 }
 
-// exp and 1 / x as the precision of the key asks for.  fp32: the hardware's exp2 and
-// reciprocal, whose error kMargin covers.
-__device__ __forceinline__ float key_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
-__device__ __forceinline__ double key_exp(double x) { return exp(x); }
-__device__ __forceinline__ float key_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
-__device__ __forceinline__ double key_rcp(double x) { return 1.0 / x; }
+// The hardware's exp2 and reciprocal, whose error margin_of covers.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
-// fp64 keys are compared as multiples of 2^-44: sums of two scores that are equal in
-// exact arithmetic, as sigmoid(x) + sigmoid(-x) for every x, then tie, and adding two
-// such keys rounds nothing more.
-__device__ __forceinline__ float on_grid(float key) { return key; }
-__device__ __forceinline__ double on_grid(double key) { return rint(key * 0x1p44) * 0x1p-44; }
-
-// Keys p + bias.  Error of the fp32 ones, with u = 2^-24: the rounded exponent makes
-// exp(x) off by 2 u |x| relative to itself, exp2 and the reciprocal by 2 u each.
-// Sigmoid: p (1 - p) |x| <= 0.23 and p (1 - p) <= 0.25, so p is off by at most 5 u and
-// the key by u more per unit of its size.  Softmax: p |x - max| <= 0.37, and the sum of
-// E <= 1024 positive terms (16 per lane, then 6 steps) adds at most 22 u.  So a key is
-// within 8 u (sigmoid) or 32 u (softmax), and two sums of two keys are told apart by
-// more than four times that: 2^-19 and 2^-17.
-template <typename K, int L, int V>
-__device__ __forceinline__ void make_keys(const RouteArgs& a, int l, const float (&x)[V], K (&key)[V]) {
+// fp32 keys p + bias.  Their error, with u = 2^-24: the rounded exponent makes exp(x)
+// off by 2 u |x| relative to itself, exp2 and the reciprocal by 2 u each.  Sigmoid:
+// p (1 - p) |x| <= 0.23 and p (1 - p) <= 0.25, so p is off by at most 5 u and the key by
+// u more per unit of its size.  Softmax: p |x - max| <= 0.37, and the sum of E <= 1024
+// positive terms (16 per lane, then 6 steps) adds at most 22 u.  So a key is within 8 u
+// (sigmoid) or 32 u (softmax), and two sums of two keys are told apart by more than four
+// times that: 2^-19 and 2^-17.
+template <int L, int V>
+__device__ __forceinline__ void make_keys(const RouteArgs& a, int l, const float (&x)[V], float (&key)[V]) {
   if (a.sigmoid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = key_rcp(K(1) + key_exp(-K(x[v])));
+    for (int v = 0; v < V; ++v) key[v] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-x[v]));
   } else {
-    float m = none<float>();
+    float m = none<float>(), sum = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) m = MaxK()(m, x[v]);
     m = team_reduce<L>(m, MaxK());
-    const K most = m > none<float>() ? K(m) : K(0);
-    K sum = K(0);
+    m = m > none<float>() ? m : 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      key[v] = key_exp(K(x[v]) - most);
+      key[v] = fast_exp(x[v] - m);
       sum += key[v];
     }
-    const K r = key_rcp(team_reduce<L>(sum, AddF()));
+    const float r = __builtin_amdgcn_rcpf(team_reduce<L>(sum, AddF()));
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] *= r;
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float b = 0.f;
     const int e = expert_of<L, V>(v, l);
-    if (a.bias && e < a.E) b = counted(a.bias[e]);
-    key[v] = x[v] > none<float>() && b > none<float>() ? on_grid(key[v] + K(b)) : none<K>();
+    const float b = a.bias ? counted(a.bias[e < a.E ? e : a.E - 1]) : 0.f;
+    key[v] = x[v] > none<float>() && b > none<float>() ? key[v] + b : none<float>();
   }
 }
 
@@ -160,95 +140,246 @@ __device__ __forceinline__ K margin_of(const RouteArgs& a, K s) {
   return size * (a.sigmoid ? K(0x1p-19) : K(0x1p-17));
 }
 
-// Keeps the keys of the topk_group best groups.  `buf`: the token's own LDS, E + n_group
-// keys (one word of padding per group keeps the lanes that scan the groups on different
-// banks) and n_group scores; only this wave touches it.
-template <typename K, int L, int V, bool CHECK>
-__device__ __forceinline__ void keep_groups(const RouteArgs& a, int l, int tok, K* buf, K (&key)[V], bool& close) {
+// The key of one expert in fp64, from its logit in memory (taken seldom, so nothing is
+// kept in registers for it).  Keys are multiples of 2^-44: sums of two scores that are
+// equal in exact arithmetic, as sigmoid(x) + sigmoid(-x) for every x, then tie, and
+// adding two such keys rounds nothing more.  Bare scores: the logit itself.
+//
+// A call, not inlined: the polynomials of exp would otherwise be kept in registers
+// through the whole kernel and push its own values out.
+__device__ __attribute__((noinline)) double exact_exp(double x) { return exp(x); }
+
+struct ExactKey {
+  const RouteArgs& a;
+  int64_t base;
+  bool arith;
+  double most, sum;      // softmax
+  __device__ __forceinline__ double operator()(int e) const {
+    const double x = logit_at(a.logits, a.bf16, base + e);
+    if (!arith) return x;
+    const double b = a.bias ? (double)counted(a.bias[e]) : 0.0;
+    const double w = exact_exp(a.sigmoid ? -x : x - most);
+    const double p = a.sigmoid ? 1.0 / (1.0 + w) : w / sum;
+    return x > none<double>() && b > none<double>() ? rint((p + b) * 0x1p44) * 0x1p-44 : none<double>();
+  }
+};
+
+template <int L>
+__device__ __forceinline__ ExactKey exact_key(const RouteArgs& a, int64_t t, int l, bool arith) {
+  ExactKey k{a, t * a.E, arith, 0.0, 1.0};
+  if (arith && !a.sigmoid) {
+    float m = none<float>();
+#pragma unroll 1
+    for (int e = l; e < a.E; e += L) m = MaxK()(m, logit_at(a.logits, a.bf16, k.base + e));
+    m = team_reduce<L>(m, MaxK());
+    k.most = m > none<float>() ? m : 0.f;
+    double sum = 0.0;
+#pragma unroll 1
+    for (int e = l; e < a.E; e += L) sum += exact_exp((double)logit_at(a.logits, a.bf16, k.base + e) - k.most);
+    k.sum = team_reduce<L>(sum, AddF());
+  }
+  return k;
+}
+
+// e / (E / n_group) for e < 1024.
+struct GroupOf {
+  uint32_t magic;
+  __device__ __forceinline__ explicit GroupOf(int per) : magic(((1u << 22) + per - 1) / per) {}
+  __device__ __forceinline__ int operator()(int e) const { return (int)(((uint32_t)e * magic) >> 22); }
+};
+
+// The groups kept, as a mask (n_group <= 16), from one score per group: lane g < n_group
+// of the team holds group g's.  `near`: the first group dropped is too close to the last
+// one kept for fp32.
+template <typename K, int L, typename Score>
+__device__ __forceinline__ uint32_t best_groups(const RouteArgs& a, int l, int tok, K s, Score score, bool& near) {
+  bool keep = false;
+  int rank = 0;
+  K gap = K(3.0e38f);
+  for (int o = 0; o < a.n_group; ++o) {
+    const K other = score(o);
+    const bool ahead = other > s || (other == s && o < l);
+    rank += ahead;
+    gap = ahead && other - s < gap ? other - s : gap;
+  }
+  keep = l < a.n_group && rank < a.topk_group && s > none<K>();
+  near = l < a.n_group && rank == a.topk_group && s > none<K>() && gap <= margin_of(a, s + gap);
+  return (uint32_t)(__ballot(keep) >> (L == 64 ? 0 : tok * L)) & 0xFFFFu;
+}
+
+// From the fp32 keys, by way of the token's own LDS: E + n_group keys (one word of
+// padding per group keeps the lanes that scan the groups on different banks) and
+// n_group scores.  Only this wave touches it.
+template <int L, int V>
+__device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int l, int tok, float* buf, const float (&key)[V],
+                                                bool& near) {
   const int per = a.E / a.n_group;
-  const uint32_t magic = ((1u << 22) + per - 1) / per;   // e / per for e < 1024
-  K* score = buf + a.E + a.n_group;
+  const GroupOf group(per);
+  float* score = buf + a.E + a.n_group;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = expert_of<L, V>(v, l);
-    if (e < a.E) buf[e + (int)((e * magic) >> 22)] = key[v];
+    if (e < a.E) buf[e + group(e)] = key[v];
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  float m1 = none<float>(), m2 = none<float>();
   if (l < a.n_group) {
-    K m1 = none<K>(), m2 = none<K>();
+#pragma unroll 8
     for (int i = 0; i < per; ++i) {
-      const K x = buf[l * (per + 1) + i];
-      const K low = x < m1 ? x : m1;
+      const float x = buf[l * (per + 1) + i];
+      const float low = x < m1 ? x : m1;
       m2 = low > m2 ? low : m2;
       m1 = x > m1 ? x : m1;
     }
-    score[l] = a.group_top == 2 && m2 > none<K>() ? m1 + m2 : m1;
+    m1 = a.group_top == 2 && m2 > none<float>() ? m1 + m2 : m1;
+    score[l] = m1;
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  bool keep = false, near = false;
+  return best_groups<float, L>(a, l, tok, m1, [&](int o) { return score[o]; }, near);
+}
+
+// The same in fp64, one lane per group.
+template <int L>
+__device__ __forceinline__ uint32_t keep_groups_exactly(const RouteArgs& a, int l, int tok, const ExactKey& key) {
+  const int per = a.E / a.n_group;
+  double m1 = none<double>(), m2 = none<double>();
   if (l < a.n_group) {
-    const K s = score[l];
-    int rank = 0;
-    K gap = K(3.0e38f);
-    for (int o = 0; o < a.n_group; ++o) {
-      const K other = score[o];
-      const bool ahead = other > s || (other == s && o < l);
-      rank += ahead;
-      gap = ahead && other - s < gap ? other - s : gap;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      const double x = key(l * per + i);
+      const double low = x < m1 ? x : m1;
+      m2 = low > m2 ? low : m2;
+      m1 = x > m1 ? x : m1;
     }
-    keep = rank < a.topk_group && s > none<K>();
-    // the first group dropped against the last one kept
-    near = rank == a.topk_group && s > none<K>() && gap <= margin_of(a, s + gap);
+    m1 = a.group_top == 2 && m2 > none<double>() ? m1 + m2 : m1;
   }
-  uint32_t kept = (uint32_t)(__ballot(keep) >> (L == 64 ? 0 : tok * L)) & 0xFFFFu;   // n_group <= 16
-  if (CHECK) close |= team_any<L>(near, tok);
+  bool near;
+  return best_groups<double, L>(a, l, tok, m1, [&](int o) { return __shfl(m1, (L == 64 ? 0 : tok * L) + o, 64); }, near);
+}
+
+template <int L, int V>
+__device__ __forceinline__ void drop_groups(const RouteArgs& a, int l, uint32_t kept, float (&key)[V]) {
+  const GroupOf group(a.E / a.n_group);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = expert_of<L, V>(v, l);
-    if (e < a.E && !((kept >> ((e * magic) >> 22)) & 1)) key[v] = none<K>();
+    if (e < a.E && !((kept >> group(e)) & 1)) key[v] = none<float>();
   }
 }
 
-// The k largest keys: lane j of the team gets the j-th expert (-1: none left).  CHECK:
-// `close` tells that two neighbours of the order are too near for fp32, the first one
-// left out among them.  Two keys made of the same logit and bias are a true tie; where
-// the first ones left out tie with the last one taken, the one after them counts too.
-template <typename K, int L, int V, bool CHECK>
-__device__ __forceinline__ void choose(const RouteArgs& a, int64_t t, int l, K (&key)[V], int& id, bool& close) {
-  K last = K(0);
-  int last_e = -1;
-  bool open = CHECK;                               // the border is not settled yet
-  for (int j = 0; j < a.k || (CHECK && __any(open)); ++j) {
-    K m = key[0];
-    int mv = 0;
-#pragma unroll
-    for (int v = 1; v < V; ++v) {
-      const bool c = key[v] > m;
-      m = c ? key[v] : m;
-      mv = c ? v : mv;
-    }
-    const K top = team_reduce<L>(m, MaxK());
-    const bool any = top > none<K>();
-    const int e = (int)team_reduce<L>(any && m == top ? (uint32_t)expert_of<L, V>(mv, l) : 0xFFFFFFFFu, MinU());
-    if (CHECK && j > 0 && open) {
-      bool same = false;
-      if (any && last - top <= margin_of(a, last)) {
-        if (last == top)
-          same = logit_at(a.logits, a.bf16, t * a.E + e) == logit_at(a.logits, a.bf16, t * a.E + last_e) &&
-                 (!a.bias || counted(a.bias[e]) == counted(a.bias[last_e]));
-        close |= !same;
+// The k largest keys in k rounds of a maximum over the team, each round among those that
+// come after the last one taken: lane j gets the j-th expert (-1: none left).  For rows
+// with more candidates than the LDS list holds, as where many logits are equal.
+template <int L>
+__device__ __forceinline__ int choose_in_rounds(const RouteArgs& a, int l, uint32_t kept, const ExactKey& key) {
+  const GroupOf group(a.E / a.n_group);
+  int id = -1, last_e = -1;
+  double last = __builtin_huge_val();
+  for (int j = 0; j < a.k; ++j) {
+    double m = none<double>();
+    int me = 0;
+#pragma unroll 1
+    for (int e = l; e < a.E; e += L) {
+      const double x = (kept >> group(e)) & 1 ? key(e) : none<double>();
+      if (x > m && (x < last || (x == last && e > last_e))) {
+        m = x;
+        me = e;
       }
-      open = any && !close && (j < a.k || same);
     }
-    if (l == j && j < a.k) id = e;
-    // d equals the lane's v-th expert number less the lane's share for the taken one only
-    const int d = V >= 4 ? e - l * 4 : e - l;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (d == expert_of<L, V>(v, 0)) key[v] = none<K>();
+    const double top = team_reduce<L>(m, MaxK());
+    const bool any = top > none<double>();
+    last_e = (int)team_reduce<L>(any && m == top ? (uint32_t)me : 0xFFFFFFFFu, MinU());
     last = top;
-    last_e = e;
+    if (l == j) id = last_e;
   }
+  return id;
+}
+
+// One token's candidates in LDS.
+constexpr int kCandidates = 64;
+struct Candidate {
+  float key;
+  int expert;
+};
+struct alignas(16) Candidates {
+  Candidate list[kCandidates];
+  double exact[kCandidates];
+  int chosen[kMaxChosen];
+};
+
+// Lower bound of the k-th largest key: the k-th largest of 16 lanes' maxima (of the four
+// rows' bounds the best one).  -infinity where fewer than k lanes hold a key.
+template <int N>
+__device__ __forceinline__ int count_reaching(float m, float other_than) {
+  // lanes N, N - 1, ... 1 further along the row
+  const int here = dpp<0x120 + N>(m) >= other_than;   // row_ror N
+  if constexpr (N > 1) return here + count_reaching<N - 1>(m, other_than);
+  else return here;
+}
+template <int L, int V>
+__device__ __forceinline__ float bound_of(int k, const float (&key)[V]) {
+  float m = key[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) m = MaxK()(m, key[v]);
+  const int reaching = 1 + count_reaching<15>(m, m);
+  return team_reduce<L>(reaching >= k ? m : none<float>(), MaxK());
+}
+
+template <int L>
+__device__ __forceinline__ uint32_t team_scan(uint32_t x) {
+  if constexpr (L == 64) {
+    return wave_scan(x, AddF());
+  } else {
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, false);
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, false);
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, false);
+    return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, false);
+  }
+}
+
+// Puts the keys that reach `least` into the list; returns how many there are (they fit
+// when that is at most kCandidates).
+template <int L, int V>
+__device__ __forceinline__ int gather(const RouteArgs& a, int l, float least, const float (&key)[V], Candidates& c) {
+  uint32_t own = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) own += key[v] >= least && key[v] > none<float>();
+  const uint32_t end = team_scan<L>(own);
+  const int n = (int)team_reduce<L>(end, MaxU());
+  uint32_t at = end - own;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (key[v] >= least && key[v] > none<float>()) {
+      if (at < kCandidates) c.list[at] = Candidate{key[v], expert_of<L, V>(v, l)};
+      ++at;
+    }
+  }
+  if (l < kMaxChosen) c.chosen[l] = -1;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  return n;
+}
+
+// Ranks the n candidates of the token by key(i), ties to the lowest expert, and writes
+// down the k first.  `near` (fp32 keys): two of them are too close.
+template <typename K, int L, bool CHECK, typename Key>
+__device__ __forceinline__ void rank(const RouteArgs& a, int l, int n, Candidates& c, Key key, bool& near) {
+  for (int base = 0; __any(base < n); base += L) {
+    const int s = base + l;
+    const bool mine = s < n;
+    const K own = mine ? key(s) : none<K>();
+    const int e = mine ? c.list[s].expert : 0;
+    const K close = CHECK ? margin_of(a, own) : K(0);
+    int ahead = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const K other = key(i);
+      const int oe = c.list[i].expert;
+      ahead += other > own || (other == own && oe < e);
+      if (CHECK) near |= mine && i != s && other - own <= close && own - other <= close;
+    }
+    if (mine && ahead < a.k) c.chosen[ahead] = e;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
 // Places of the pairs of one workgroup's tokens.  base[e]: the place of the block's
@@ -329,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
   __shared__ int chosen[64 * kMaxChosen];
   __shared__ int wave_sums[kWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int l = lane % L, tok = lane / L;
+  const int tok = lane / L;
   const bool plan = a.M_sizes != nullptr;
   const bool alone = gridDim.x == 1 && a.block_tokens == 64;
   if (plan) {
@@ -340,40 +471,49 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
   const int64_t first = (int64_t)blockIdx.x * a.block_tokens;
   for (int at = wave * (64 / L); at < a.block_tokens; at += kTokens) {
     if (first + at >= a.T) break;                  // uniform over the wave
+    // Opaque to the compiler in each pass: it would keep what follows from the lane for
+    // every v (expert, group, addresses) in registers across the passes, of which there
+    // is seldom more than one.
+    int l = lane % L;
+    asm volatile("" : "+v"(l));
     const bool live = first + at + tok < a.T;
     const int64_t t = live ? first + at + tok : a.T - 1;
     float x[V];
     load_row<L, V>(a, t, l, x);
-    int id = -1;
-    bool close = false;
+    char* own_lds = reinterpret_cast<char*>(dynamic_lds) + (wave * (64 / L) + tok) * a.token_lds;
+    Candidates& list = *reinterpret_cast<Candidates*>(own_lds);
+    float key[V];
+    uint32_t kept = 0xFFFFu;
     if constexpr (ARITH) {
-      const int region = a.E + 2 * a.n_group + 1;
-      float key[V];
-      make_keys<float, L, V>(a, l, x, key);
-      if (a.n_group > 1)
-        keep_groups<float, L, V, true>(a, l, tok, reinterpret_cast<float*>(dynamic_lds + (wave * (64 / L) + tok) * region),
-                                       key, close);
-      choose<float, L, V, true>(a, t, l, key, id, close);
-      if (__any(close)) {
-        double exact[V];
-        int exact_id = -1;
-        bool unused = false;
-        make_keys<double, L, V>(a, l, x, exact);
-        if (a.n_group > 1)
-          keep_groups<double, L, V, false>(a, l, tok, dynamic_lds + (wave * (64 / L) + tok) * region, exact, unused);
-        choose<double, L, V, false>(a, t, l, exact, exact_id, unused);
-        if (close) id = exact_id;
-      }
+      make_keys<L, V>(a, l, x, key);
     } else {
-      bool unused = false;
-      float key[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) key[v] = x[v];
-      if (a.n_group > 1)
-        keep_groups<float, L, V, false>(
-            a, l, tok, reinterpret_cast<float*>(dynamic_lds) + (wave * (64 / L) + tok) * (a.E + 2 * a.n_group + 1), key,
-            unused);
-      choose<float, L, V, false>(a, t, l, key, id, unused);
+    }
+    if (a.n_group > 1) {
+      bool near = false;
+      kept = keep_groups<L, V>(a, l, tok, reinterpret_cast<float*>(own_lds), key, near);
+      if (ARITH && __any(near)) kept = keep_groups_exactly<L>(a, l, tok, exact_key<L>(a, t, l, true));
+      drop_groups<L, V>(a, l, kept, key);
+    }
+    const float bound = bound_of<L, V>(a.k, key);
+    const int n = gather<L, V>(a, l, ARITH ? bound - margin_of(a, bound) : bound, key, list);
+    const int listed = n < kCandidates ? n : kCandidates;
+    bool near = false;
+    rank<float, L, ARITH>(a, l, listed, list, [&](int i) { return list.list[i].key; }, near);
+    if constexpr (ARITH) {
+      if (__any(near && n <= kCandidates)) {
+        const ExactKey exact = exact_key<L>(a, t, l, true);
+        for (int i = l; i < listed; i += L) list.exact[i] = exact(list.list[i].expert);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        rank<double, L, false>(a, l, listed, list, [&](int i) { return list.exact[i]; }, near);
+      }
+    }
+    int id = -1;
+    if (l < a.k) id = list.chosen[l];
+    if (__any(n > kCandidates)) {
+      const int in_rounds = choose_in_rounds<L>(a, l, kept, exact_key<L>(a, t, l, ARITH));
+      if (n > kCandidates) id = in_rounds;
     }
     // Weights: lane j has the j-th expert; all of them lie in the team's first 16 lanes.
     const bool mine = l < a.k && id >= 0;
@@ -426,9 +566,12 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
               a.dst_row);
 }
 
-// Second kernel of the plan: block b adds up the counts of all blocks and of those
-// before it, then places its own pairs.
-__global__ void __launch_bounds__(kThreads) place_kernel(RouteArgs a, int blocks) {
+// Second kernel of the plan: each workgroup takes the pairs of `span` neighbouring blocks
+// of the first one; it adds up the counts of all blocks and of those before its own,
+// then places its pairs.  At most 64 workgroups, because each of them reads all counts
+// (256 x 256 of them at 16384 tokens and 256 experts: one workgroup per block took 21 us).
+constexpr int kPlaceGroups = 64;
+__global__ void __launch_bounds__(kThreads) place_kernel(RouteArgs a, int blocks, int span) {
   extern __shared__ double dynamic_lds[];
   __shared__ int total[kMaxExperts];
   __shared__ int earlier[kMaxExperts];
@@ -439,12 +582,18 @@ __global__ void __launch_bounds__(kThreads) place_kernel(RouteArgs a, int blocks
   // lanes of experts side by side, as many rows of counts at once as fit
   const int width = a.E <= 64 ? 64 : (a.E <= 128 ? 128 : (a.E <= 256 ? 256 : (a.E <= 512 ? 512 : 1024)));
   const int e = threadIdx.x % width, step = kThreads / width;
+  const int first_block = blockIdx.x * span;
   if (e < a.E) {
     int all = 0, prior = 0;
-    for (int b = threadIdx.x / width; b < blocks; b += step) {
-      const int c = a.hist[(int64_t)b * a.E + e];
-      all += c;
-      prior += b < (int)blockIdx.x ? c : 0;
+    for (int b = threadIdx.x / width; b < blocks; b += 8 * step) {
+      int c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = b + i * step < blocks ? a.hist[(int64_t)(b + i * step) * a.E + e] : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        all += c[i];
+        prior += b + i * step < first_block ? c[i] : 0;
+      }
     }
     atomicAdd(&total[e], all);
     atomicAdd(&earlier[e], prior);
@@ -455,9 +604,8 @@ __global__ void __launch_bounds__(kThreads) place_kernel(RouteArgs a, int blocks
   if (blockIdx.x == 0 && (int)threadIdx.x < a.E) a.M_sizes[threadIdx.x] = c;
   earlier[threadIdx.x] += before;
   __syncthreads();
-  const int64_t first = (int64_t)blockIdx.x * a.block_tokens;
-  const int64_t left = a.T - first;
-  const int n = (int)(left < a.block_tokens ? left : a.block_tokens) * a.k;
+  const int64_t first = (int64_t)first_block * a.block_tokens, most = (int64_t)span * a.block_tokens;
+  const int n = (int)(a.T - first < most ? a.T - first : most) * a.k;
   const int32_t* ids = a.ids + first * a.k;
   place_pairs([&](int i) { return ids[i]; }, n, a.E, earlier, reinterpret_cast<int*>(dynamic_lds),
               a.dst_row + first * a.k);
@@ -465,10 +613,14 @@ __global__ void __launch_bounds__(kThreads) place_kernel(RouteArgs a, int blocks
 
 template <int L, int V, bool ARITH>
 hipError_t launch(const RouteArgs& a, int blocks, hipStream_t stream) {
-  const size_t keys = a.n_group > 1 ? (size_t)kWaves * (64 / L) * (a.E + 2 * a.n_group + 1) * (ARITH ? 8 : 4) : 0;
+  // a token's candidates, and before them its keys by group, in the same place
+  const int keys = a.n_group > 1 ? (a.E + 2 * a.n_group) * (int)sizeof(float) : 0;
+  RouteArgs b = a;
+  b.token_lds = ((keys > (int)sizeof(Candidates) ? keys : (int)sizeof(Candidates)) + 15) / 16 * 16;
+  const size_t tokens = (size_t)kWaves * (64 / L) * b.token_lds;
   const size_t counts = a.M_sizes && blocks == 1 ? (size_t)kWaves * a.E * sizeof(int) : 0;
-  const size_t lds = keys > counts ? keys : counts;
-  hipLaunchKernelGGL((route_kernel<L, V, ARITH>), dim3(blocks), dim3(kThreads), lds, stream, a);
+  hipLaunchKernelGGL((route_kernel<L, V, ARITH>), dim3(blocks), dim3(kThreads), tokens > counts ? tokens : counts, stream,
+                     b);
   return hipGetLastError();
 }
 
@@ -579,7 +731,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
   const bool arith = a.bias || (a.n_group > 1 && a.group_top == 2);
   hipError_t e = arith ? launch_by_width<true>(a, blocks, stream) : launch_by_width<false>(a, blocks, stream);
   if (e != hipSuccess || !a.M_sizes || blocks == 1) return e;
-  hipLaunchKernelGGL(place_kernel, dim3(blocks), dim3(kThreads), (size_t)kWaves * a.E * sizeof(int), stream, a, blocks);
+  const int span = (blocks + kPlaceGroups - 1) / kPlaceGroups;
+  hipLaunchKernelGGL(place_kernel, dim3((blocks + span - 1) / span), dim3(kThreads), (size_t)kWaves * a.E * sizeof(int),
+                     stream, a, blocks, span);
   return hipGetLastError();
 }
 
