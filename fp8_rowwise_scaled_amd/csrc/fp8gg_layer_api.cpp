@@ -234,7 +234,7 @@ fp8gg_status f8f8bf16_route(const void* logits, int logits_dtype, const float* b
                    {"ids", ids, 4 * T * k, 4, true, false},
                    {"M_sizes", M_sizes, 8 * E, 8, true, true},
                    {"dst_row", dst_row, 4 * T * k, 4, true, true},
-                   {"workspace", workspace, need, 4, true, true}}));
+                   {"workspace", workspace, need, 16, true, true}}));
   const fp8gg::RouteArgs a{logits, bias, weights, ids, M_sizes, dst_row, static_cast<int32_t*>(workspace), T,
                            (int32_t)E, (int32_t)k, (int32_t)n_group, (int32_t)topk_group, group_top,
                            logits_dtype == FP8GG_DTYPE_BF16, score == FP8GG_SCORE_SIGMOID, renormalize != 0,

@@ -42,14 +42,12 @@ __device__ __forceinline__ T team_reduce(T x, Op op) {
   else return wave_reduce(x, op);
 }
 
-// The expert of the lane's v-th key.  From four keys per lane on, four neighbouring
-// experts sit in one lane, so that a row is read with 16-byte (bf16: 8-byte) loads.
-// Expert numbers rise with v within a lane.
-template <int L, int V>
-__device__ __forceinline__ int expert_of(int v, int l) {
-  if constexpr (V >= 4) return (v >> 2) * (4 * L) + l * 4 + (v & 3);
-  else return v * L + l;
-}
+// The expert of the lane's v-th key: neighbouring experts lie in neighbouring lanes, so
+// that every lane has its share of each group of experts.  (With four neighbours per
+// lane, for wider loads, kept groups may leave half the lanes without a key: the
+// bound below falls and the list of candidates grows, to 60 of them now and then.)
+template <int L>
+__device__ __forceinline__ int expert_of(int v, int l) { return v * L + l; }
 
 template <typename T>
 __device__ __forceinline__ T none() { return -__builtin_huge_valf(); }
@@ -68,31 +66,15 @@ __device__ __forceinline__ float logit_at(const void* logits, int bf16, int64_t 
 template <int L, int V>
 __device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int l, float (&x)[V]) {
   const int64_t base = t * a.E;
-  if constexpr (V >= 4) {
-    if (a.E % 4 == 0) {
+  if (a.E == L * V) {   // no lane past the last expert
 #pragma unroll
-      for (int v = 0; v < V; v += 4) {
-        const int e = expert_of<L, V>(v, l);
-        f32x4 w = {none<float>(), none<float>(), none<float>(), none<float>()};
-        if (e < a.E) {
-          if (a.bf16) {
-            const u32x2 q = *reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(a.logits) + base + e);
-            w = f32x4{__uint_as_float(q[0] << 16), __uint_as_float(q[0] & 0xFFFF0000u), __uint_as_float(q[1] << 16),
-                      __uint_as_float(q[1] & 0xFFFF0000u)};
-          } else {
-            w = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(a.logits) + base + e);
-          }
-        }
+    for (int v = 0; v < V; ++v) x[v] = logit_at(a.logits, a.bf16, base + expert_of<L>(v, l));
+  } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[v + i] = counted(w[i]);
-      }
-      return;
+    for (int v = 0; v < V; ++v) {
+      const int e = expert_of<L>(v, l);
+      x[v] = e < a.E ? logit_at(a.logits, a.bf16, base + e) : none<float>();
     }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = expert_of<L, V>(v, l);
-    x[v] = e < a.E ? logit_at(a.logits, a.bf16, base + e) : none<float>();
   }
 }
 
@@ -128,7 +110,7 @@ __device__ __forceinline__ void make_keys(const RouteArgs& a, int l, const float
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = expert_of<L, V>(v, l);
+    const int e = expert_of<L>(v, l);
     const float b = a.bias ? counted(a.bias[e < a.E ? e : a.E - 1]) : 0.f;
     key[v] = x[v] > none<float>() && b > none<float>() ? key[v] + b : none<float>();
   }
@@ -185,76 +167,130 @@ __device__ __forceinline__ ExactKey exact_key(const RouteArgs& a, int64_t t, int
 struct GroupOf {
   uint32_t magic;
   __device__ __forceinline__ explicit GroupOf(int per) : magic(((1u << 22) + per - 1) / per) {}
-  __device__ __forceinline__ int operator()(int e) const { return (int)(((uint32_t)e * magic) >> 22); }
+  __device__ __forceinline__ int operator()(int e) const { return (int)(__umul24((uint32_t)e, magic) >> 22); }
 };
 
-// The groups kept, as a mask (n_group <= 16), from one score per group: lane g < n_group
-// of the team holds group g's.  `near`: the first group dropped is too close to the last
-// one kept for fp32.
-template <typename K, int L, typename Score>
-__device__ __forceinline__ uint32_t best_groups(const RouteArgs& a, int l, int tok, K s, Score score, bool& near) {
-  bool keep = false;
-  int rank = 0;
-  K gap = K(3.0e38f);
-  for (int o = 0; o < a.n_group; ++o) {
-    const K other = score(o);
-    const bool ahead = other > s || (other == s && o < l);
-    rank += ahead;
-    gap = ahead && other - s < gap ? other - s : gap;
-  }
-  keep = l < a.n_group && rank < a.topk_group && s > none<K>();
-  near = l < a.n_group && rank == a.topk_group && s > none<K>() && gap <= margin_of(a, s + gap);
-  return (uint32_t)(__ballot(keep) >> (L == 64 ? 0 : tok * L)) & 0xFFFFu;
+constexpr int kMaxGroups = 16;
+
+// The groups kept, as a mask, from lane g's (g < n_group) score, its rank and its distance
+// to the nearest score ahead of it.  `near`: the first group dropped is too close to the
+// last one kept for fp32.
+template <typename K, int L>
+__device__ __forceinline__ uint32_t groups_within(const RouteArgs& a, int l, int tok, K s, int rank, K gap, bool& near) {
+  const bool real = l < a.n_group && s > none<K>();
+  near = real && rank == a.topk_group && gap <= margin_of(a, s + gap);
+  return (uint32_t)(__ballot(real && rank < a.topk_group) >> (L == 64 ? 0 : tok * L)) & 0xFFFFu;
 }
 
-// From the fp32 keys, by way of the token's own LDS: E + n_group keys (one word of
-// padding per group keeps the lanes that scan the groups on different banks) and
-// n_group scores.  Only this wave touches it.
-template <int L, int V>
-__device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int l, int tok, float* buf, const float (&key)[V],
-                                                bool& near) {
-  const int per = a.E / a.n_group;
-  const GroupOf group(per);
-  float* score = buf + a.E + a.n_group;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = expert_of<L, V>(v, l);
-    if (e < a.E) buf[e + group(e)] = key[v];
-  }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  float m1 = none<float>(), m2 = none<float>();
-  if (l < a.n_group) {
-#pragma unroll 8
-    for (int i = 0; i < per; ++i) {
-      const float x = buf[l * (per + 1) + i];
-      const float low = x < m1 ? x : m1;
-      m2 = low > m2 ? low : m2;
-      m1 = x > m1 ? x : m1;
-    }
-    m1 = a.group_top == 2 && m2 > none<float>() ? m1 + m2 : m1;
-    score[l] = m1;
-  }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  return best_groups<float, L>(a, l, tok, m1, [&](int o) { return score[o]; }, near);
-}
-
-// The same in fp64, one lane per group.
+// Group l's score in fp64, one lane per group, from the experts whose fp32 key reaches
+// `least` (the second one's less the error bound): nearly always the two that count, so
+// they are listed first and their scores computed side by side.
 template <int L>
-__device__ __forceinline__ uint32_t keep_groups_exactly(const RouteArgs& a, int l, int tok, const ExactKey& key) {
+__device__ __forceinline__ uint32_t keep_groups_exactly(const RouteArgs& a, int l, int tok, const float* buf, float least,
+                                                        const ExactKey& key) {
+  constexpr int kListed = 4;
   const int per = a.E / a.n_group;
-  double m1 = none<double>(), m2 = none<double>();
+  const float* own = buf + l * (per + 1);
+  int list[kListed] = {}, n = 0;
   if (l < a.n_group) {
-#pragma unroll 1
     for (int i = 0; i < per; ++i) {
-      const double x = key(l * per + i);
-      const double low = x < m1 ? x : m1;
-      m2 = low > m2 ? low : m2;
-      m1 = x > m1 ? x : m1;
+      if (own[i] < least || !(own[i] > none<float>())) continue;
+#pragma unroll
+      for (int u = 0; u < kListed; ++u)
+        if (u == n) list[u] = i;
+      ++n;
     }
-    m1 = a.group_top == 2 && m2 > none<double>() ? m1 + m2 : m1;
+  }
+  double m1 = none<double>(), m2 = none<double>();
+  const auto take = [&](double x) {
+    const double low = x < m1 ? x : m1;
+    m2 = low > m2 ? low : m2;
+    m1 = x > m1 ? x : m1;
+  };
+#pragma unroll
+  for (int u = 0; u < kListed; ++u)
+    if (u < n && n <= kListed) take(key(l * per + list[u]));
+  if (n > kListed) {
+#pragma unroll 1
+    for (int i = 0; i < per; ++i)
+      if (own[i] >= least) take(key(l * per + i));
+  }
+  if (a.group_top == 2 && m2 > none<double>()) m1 += m2;
+  int rank = 0;
+  for (int o = 0; o < a.n_group; ++o) {
+    const double other = __shfl(m1, (L == 64 ? 0 : tok * L) + o, 64);
+    rank += other > m1 || (other == m1 && o < l);
   }
   bool near;
-  return best_groups<double, L>(a, l, tok, m1, [&](int o) { return __shfl(m1, (L == 64 ? 0 : tok * L) + o, 64); }, near);
+  return groups_within<double, L>(a, l, tok, m1, rank, 0.0, near);
+}
+
+// The groups kept, by way of the token's own LDS: kMaxGroups best and second keys and E +
+// n_group keys (one word of padding per group keeps the lanes that scan the groups on
+// different banks).  Only this wave touches it.  Two lanes scan a group where there are
+// enough.  ARITH: the keys are fp32 sums, and a border too close is decided in fp64.
+template <int L, int V, bool ARITH>
+__device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int64_t t, int l, int tok, float* lds,
+                                                const float (&key)[V]) {
+  const int per = a.E / a.n_group;
+  const GroupOf group(per);
+  float *best = lds, *second = lds + kMaxGroups, *buf = lds + 2 * kMaxGroups;
+  if (a.E == L * V) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) buf[expert_of<L>(v, l) + group(expert_of<L>(v, l))] = key[v];
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (expert_of<L>(v, l) < a.E) buf[expert_of<L>(v, l) + group(expert_of<L>(v, l))] = key[v];
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  const bool pairs = 2 * a.n_group <= L;
+  const int g = pairs ? l >> 1 : l, step = pairs ? 2 : 1;
+  float m1 = none<float>(), m2 = none<float>();
+  const auto take = [&](float x) {
+    const float low = x < m1 ? x : m1;
+    m2 = low > m2 ? low : m2;
+    m1 = x > m1 ? x : m1;
+  };
+  if (g < a.n_group) {
+#pragma unroll 8
+    for (int i = pairs ? l & 1 : 0; i < per; i += step) take(buf[g * (per + 1) + i]);
+  }
+  if (pairs) {
+    const float o1 = dpp<0xB1>(m1), o2 = dpp<0xB1>(m2);
+    take(o1);
+    m2 = o2 > m2 ? o2 : m2;
+  }
+  if (g < a.n_group) {
+    best[g] = a.group_top == 2 && m2 > none<float>() ? m1 + m2 : m1;
+    second[g] = a.group_top == 2 && m2 > none<float>() ? m2 : m1;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  const float mine = l < a.n_group ? best[l] : none<float>();
+  // all scores at once: a read per step of the loop would wait for LDS each time
+  f32x4 all[kMaxGroups / 4];
+#pragma unroll
+  for (int i = 0; i < kMaxGroups / 4; ++i) all[i] = reinterpret_cast<const f32x4*>(best)[i];
+  int rank = 0;
+  float gap = 3.0e38f;
+#pragma unroll
+  for (int o = 0; o < kMaxGroups; ++o) {
+    if (o >= a.n_group) break;
+    const float other = all[o / 4][o % 4];
+    const bool ahead = other > mine || (other == mine && o < l);
+    rank += ahead;
+    const float above = ahead ? other - mine : gap;
+    gap = above < gap ? above : gap;
+  }
+  bool near;
+  uint32_t kept = groups_within<float, L>(a, l, tok, mine, rank, gap, near);
+  if constexpr (ARITH) {
+    if (__any(near)) {
+      const float low = l < a.n_group ? second[l] : none<float>();
+      kept = keep_groups_exactly<L>(a, l, tok, buf, low - margin_of(a, low), exact_key<L>(a, t, l, true));
+    }
+  }
+  return kept;
 }
 
 template <int L, int V>
@@ -262,7 +298,7 @@ __device__ __forceinline__ void drop_groups(const RouteArgs& a, int l, uint32_t 
   const GroupOf group(a.E / a.n_group);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = expert_of<L, V>(v, l);
+    const int e = expert_of<L>(v, l);
     if (e < a.E && !((kept >> group(e)) & 1)) key[v] = none<float>();
   }
 }
@@ -297,12 +333,9 @@ __device__ __forceinline__ int choose_in_rounds(const RouteArgs& a, int l, uint3
 
 // One token's candidates in LDS.
 constexpr int kCandidates = 64;
-struct Candidate {
-  float key;
-  int expert;
-};
 struct alignas(16) Candidates {
-  Candidate list[kCandidates];
+  float key[kCandidates];
+  int expert[kCandidates];
   double exact[kCandidates];
   int chosen[kMaxChosen];
 };
@@ -350,84 +383,118 @@ __device__ __forceinline__ int gather(const RouteArgs& a, int l, float least, co
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (key[v] >= least && key[v] > none<float>()) {
-      if (at < kCandidates) c.list[at] = Candidate{key[v], expert_of<L, V>(v, l)};
+      if (at < kCandidates) {
+        c.key[at] = key[v];
+        c.expert[at] = expert_of<L>(v, l);
+      }
       ++at;
     }
+  }
+  if (l < 4 && n + l < kCandidates) {              // read four at a time
+    c.key[n + l] = none<float>();
+    c.expert[n + l] = a.E;
   }
   if (l < kMaxChosen) c.chosen[l] = -1;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   return n;
 }
 
-// Ranks the n candidates of the token by key(i), ties to the lowest expert, and writes
-// down the k first.  `near` (fp32 keys): two of them are too close.
-template <typename K, int L, bool CHECK, typename Key>
-__device__ __forceinline__ void rank(const RouteArgs& a, int l, int n, Candidates& c, Key key, bool& near) {
+// Ranks the n candidates of the token by their fp32 keys and writes down the k first.
+// CHECK: `near` tells that two keys are too close (equal ones among them: their order is
+// left open).  Else ties go to the lowest expert.
+template <int L, bool CHECK>
+__device__ __forceinline__ void rank(const RouteArgs& a, int l, int n, Candidates& c, bool& near) {
   for (int base = 0; __any(base < n); base += L) {
     const int s = base + l;
     const bool mine = s < n;
-    const K own = mine ? key(s) : none<K>();
-    const int e = mine ? c.list[s].expert : 0;
-    const K close = CHECK ? margin_of(a, own) : K(0);
-    int ahead = 0;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const K other = key(i);
-      const int oe = c.list[i].expert;
-      ahead += other > own || (other == own && oe < e);
-      if (CHECK) near |= mine && i != s && other - own <= close && own - other <= close;
+    const float own = mine ? c.key[s] : none<float>();
+    const int e = mine ? c.expert[s] : 0;
+    const float close = margin_of(a, own);
+    int ahead = 0, around = 0;
+    for (int i = 0; i < n; i += 4) {
+      const f32x4 other = *reinterpret_cast<const f32x4*>(c.key + i);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (CHECK) {
+          ahead += other[u] > own;
+          around += fabsf(other[u] - own) <= close;
+        } else {
+          ahead += other[u] > own || (other[u] == own && c.expert[i + u] < e);
+        }
+      }
     }
+    if (CHECK) near |= mine && around > 1;
     if (mine && ahead < a.k) c.chosen[ahead] = e;
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
+// The same by their fp64 keys.
+template <int L>
+__device__ __forceinline__ void rank_exactly(const RouteArgs& a, int l, int n, Candidates& c, const ExactKey& key) {
+  for (int i = l; i < n; i += L) c.exact[i] = key(c.expert[i]);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  for (int s = l; s < n; s += L) {
+    const double own = c.exact[s];
+    const int e = c.expert[s];
+    int ahead = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) ahead += c.exact[i] > own || (c.exact[i] == own && c.expert[i] < e);
+    if (ahead < a.k) c.chosen[ahead] = e;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // Places of the pairs of one workgroup's tokens.  base[e]: the place of the block's
-// first pair of expert e.  Every wave walks a run of 64-pair pieces: first to count,
-// then, from the counts of the waves before it, to rank.
+// first pair of expert e.  Every wave takes a run of 64-pair pieces: it counts them, and
+// ranks them from the counts of the waves before it.
 template <typename Ids>
 __device__ __forceinline__ void place_pairs(Ids ids, int n, int E, const int* base, int* counts, int32_t* dst) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int pieces = (n + 63) / 64;
   const int per_wave = (pieces + kWaves - 1) / kWaves;
+  const int first = wave * per_wave, end = first + per_wave < pieces ? first + per_wave : pieces;
   const int bits = 32 - __clz(E);                    // E itself marks a slot without an expert
   int* own = counts + wave * E;
   for (int i = threadIdx.x; i < kWaves * E; i += kThreads) counts[i] = 0;
   __syncthreads();
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int p = wave * per_wave; p < (wave + 1) * per_wave && p < pieces; ++p) {
-      const int i = p * 64 + lane;
-      int e = i < n ? ids(i) : E;
-      if (e < 0) e = E;
-      uint64_t same = ~uint64_t(0);
-      for (int b = 0; b < bits; ++b) {
-        const bool one = (e >> b) & 1;
-        const uint64_t with = __ballot(one);
-        same &= one ? with : ~with;
-      }
-      const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
-      if (e < E) {
-        const int at = own[e];
-        if (pass) dst[i] = at + before;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (before == 0) own[e] = at + __popcll(same);
-      } else if (pass && i < n) {
-        dst[i] = -1;
-      }
+  for (int p = first; p < end; ++p) {
+    const int i = p * 64 + lane;
+    const int e = i < n ? ids(i) : -1;
+    if (e >= 0) atomicAdd(&own[e], 1);
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < E) {
+    int c[kWaves], at = base[threadIdx.x];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) c[w] = counts[w * E + threadIdx.x];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      counts[w * E + threadIdx.x] = at;
+      at += c[w];
+    }
+  }
+  __syncthreads();
+  for (int p = first; p < end; ++p) {
+    const int i = p * 64 + lane;
+    const int id = i < n ? ids(i) : -1;
+    const int e = id < 0 ? E : id;
+    uint64_t same = ~uint64_t(0);
+    for (int b = 0; b < bits; ++b) {
+      const bool one = (e >> b) & 1;
+      const uint64_t with = __ballot(one);
+      same &= one ? with : ~with;
+    }
+    const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
+    if (e < E) {
+      const int at = own[e];
+      dst[i] = at + before;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (before == 0) own[e] = at + __popcll(same);
+    } else if (i < n) {
+      dst[i] = -1;
     }
-    __syncthreads();
-    if (pass == 0) {
-      if ((int)threadIdx.x < E) {
-        int at = base[threadIdx.x];
-        for (int w = 0; w < kWaves; ++w) {
-          const int c = counts[w * E + threadIdx.x];
-          counts[w * E + threadIdx.x] = at;
-          at += c;
-        }
-      }
-      __syncthreads();
-    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
 
@@ -491,23 +558,16 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
       for (int v = 0; v < V; ++v) key[v] = x[v];
     }
     if (a.n_group > 1) {
-      bool near = false;
-      kept = keep_groups<L, V>(a, l, tok, reinterpret_cast<float*>(own_lds), key, near);
-      if (ARITH && __any(near)) kept = keep_groups_exactly<L>(a, l, tok, exact_key<L>(a, t, l, true));
+      kept = keep_groups<L, V, ARITH>(a, t, l, tok, reinterpret_cast<float*>(own_lds), key);
       drop_groups<L, V>(a, l, kept, key);
     }
     const float bound = bound_of<L, V>(a.k, key);
     const int n = gather<L, V>(a, l, ARITH ? bound - margin_of(a, bound) : bound, key, list);
     const int listed = n < kCandidates ? n : kCandidates;
     bool near = false;
-    rank<float, L, ARITH>(a, l, listed, list, [&](int i) { return list.list[i].key; }, near);
+    rank<L, ARITH>(a, l, listed, list, near);
     if constexpr (ARITH) {
-      if (__any(near && n <= kCandidates)) {
-        const ExactKey exact = exact_key<L>(a, t, l, true);
-        for (int i = l; i < listed; i += L) list.exact[i] = exact(list.list[i].expert);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        rank<double, L, false>(a, l, listed, list, [&](int i) { return list.exact[i]; }, near);
-      }
+      if (__any(near && n <= kCandidates)) rank_exactly<L>(a, l, listed, list, exact_key<L>(a, t, l, true));
     }
     int id = -1;
     if (l < a.k) id = list.chosen[l];
@@ -579,18 +639,42 @@ __global__ void __launch_bounds__(kThreads) place_kernel(RouteArgs a, int blocks
   total[threadIdx.x] = 0;
   earlier[threadIdx.x] = 0;
   __syncthreads();
-  // lanes of experts side by side, as many rows of counts at once as fit
-  const int width = a.E <= 64 ? 64 : (a.E <= 128 ? 128 : (a.E <= 256 ? 256 : (a.E <= 512 ? 512 : 1024)));
-  const int e = threadIdx.x % width, step = kThreads / width;
+  // lanes of experts side by side, as many rows of counts at once as fit; four experts
+  // per lane where the rows allow it
   const int first_block = blockIdx.x * span;
-  if (e < a.E) {
+  const int lanes = a.E % 4 == 0 ? a.E / 4 : a.E;
+  int width = 1;
+  while (width < lanes) width *= 2;
+  const int step = kThreads / width;
+  const int e = threadIdx.x % width;
+  if (a.E % 4 == 0 && e < lanes) {
+    u32x4 all = {0, 0, 0, 0}, prior = {0, 0, 0, 0};
+    for (int b = threadIdx.x / width; b < blocks; b += 16 * step) {
+      u32x4 c[16];                                 // sixteen loads in flight
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        c[i] = u32x4{0, 0, 0, 0};
+        if (b + i * step < blocks) c[i] = reinterpret_cast<const u32x4*>(a.hist + (int64_t)(b + i * step) * a.E)[e];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        all += c[i];
+        if (b + i * step < first_block) prior += c[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      atomicAdd(&total[4 * e + i], (int)all[i]);
+      atomicAdd(&earlier[4 * e + i], (int)prior[i]);
+    }
+  } else if (a.E % 4 != 0 && e < a.E) {
     int all = 0, prior = 0;
-    for (int b = threadIdx.x / width; b < blocks; b += 8 * step) {
-      int c[8];
+    for (int b = threadIdx.x / width; b < blocks; b += 16 * step) {
+      int c[16];                                   // sixteen loads in flight
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = b + i * step < blocks ? a.hist[(int64_t)(b + i * step) * a.E + e] : 0;
+      for (int i = 0; i < 16; ++i) c[i] = b + i * step < blocks ? a.hist[(int64_t)(b + i * step) * a.E + e] : 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 16; ++i) {
         all += c[i];
         prior += b + i * step < first_block ? c[i] : 0;
       }
@@ -614,7 +698,7 @@ __global__ void __launch_bounds__(kThreads) place_kernel(RouteArgs a, int blocks
 template <int L, int V, bool ARITH>
 hipError_t launch(const RouteArgs& a, int blocks, hipStream_t stream) {
   // a token's candidates, and before them its keys by group, in the same place
-  const int keys = a.n_group > 1 ? (a.E + 2 * a.n_group) * (int)sizeof(float) : 0;
+  const int keys = a.n_group > 1 ? (2 * kMaxGroups + a.E + a.n_group) * (int)sizeof(float) : 0;
   RouteArgs b = a;
   b.token_lds = ((keys > (int)sizeof(Candidates) ? keys : (int)sizeof(Candidates)) + 15) / 16 * 16;
   const size_t tokens = (size_t)kWaves * (64 / L) * b.token_lds;

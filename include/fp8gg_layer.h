@@ -125,7 +125,7 @@ int64_t f8f8bf16_rmsnorm_backward_workspace(int64_t rows, int64_t K);
  *   dst_row   [T, k]   int32: the row of pair (t, j) when pairs are sorted by expert, and
  *                      within an expert by t, then j
  *   M_sizes and dst_row may both be NULL (no plan).
- *   workspace          f8f8bf16_route_workspace(T, E, k) bytes, 4-byte aligned; may be
+ *   workspace          f8f8bf16_route_workspace(T, E, k) bytes, 16-byte aligned; may be
  *                      NULL when that is 0 or there is no plan
  *
  * 1 <= k <= 16, k <= E <= 1024, E % n_group == 0, n_group <= 16,
