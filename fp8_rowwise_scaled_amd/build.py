@@ -1,4 +1,5 @@
-"""Builds the HIP library libfp8gg.so (gfx950) in place, next to this file.
+"""Builds the HIP library libfp8gg.so (gfx950) and the binding of the layer operators,
+_layer_binding.so, in place, next to this file.
 
     python -m fp8_rowwise_scaled_amd.build [-v]
 """
@@ -15,6 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8gg.so")
+BINDING_SRC = os.path.join(PKG, "binding", "layer_binding.cpp")
+BINDING = os.path.join(PKG, "_layer_binding.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
@@ -38,8 +41,41 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".hip", ".cpp")))
 
 
+def compile_binding(obj: str) -> str:
+    """Compile the CPython module against this interpreter's torch (host code only)."""
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", "/opt/rocm/include", "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}{r.stderr}")
+    return obj
+
+
+def link_binding(obj: str) -> str:
+    """Link the module with torch and with the library beside it."""
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, "-L", libs, "-lc10", "-lc10_hip", "-ltorch_cpu",
+           "-ltorch_python", "-L", PKG, "-l:libfp8gg.so", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile every source under csrc/ and link libfp8gg.so.  Always rebuilds."""
+    """Compile every source under csrc/ and the binding; link libfp8gg.so and
+    _layer_binding.so.  Always rebuilds."""
     hipcc = _hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
@@ -57,16 +93,20 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
             print(out)
         return obj
 
-    with ThreadPoolExecutor(max(1, min(8, len(srcs)))) as ex:
+    binding_obj = os.path.join(BUILD_DIR, "layer_binding.o")
+    with ThreadPoolExecutor(max(1, min(8, len(srcs) + 1))) as ex:
+        binding = ex.submit(compile_binding, binding_obj)
         list(ex.map(compile_one, zip(srcs, objs)))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB)
+    link_binding(binding_obj)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {BINDING}")
     return LIB
 
 
