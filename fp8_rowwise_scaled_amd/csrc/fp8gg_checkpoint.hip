@@ -22,6 +22,20 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
 }
 
+template <bool STREAM, int TPR, int NV>
+__device__ __forceinline__ void load_halves(const SiluArgs& a, int64_t row, int lane, u32x4 (&rg)[NV], u32x4 (&ru)[NV]) {
+  const int nvec = a.I / 8;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = i * TPR + lane;
+    rg[i] = ru[i] = u32x4{0, 0, 0, 0};
+    if (j < nvec) {
+      rg[i] = load_in<STREAM>(reinterpret_cast<const u32x4*>(a.H) + 2 * row * nvec + j);
+      ru[i] = load_in<STREAM>(reinterpret_cast<const u32x4*>(a.H) + (2 * row + 1) * nvec + j);
+    }
+  }
+}
+
 // A team of TPR threads works on one row, NV x 8 columns of each half per thread.
 template <int TPR, int NV, bool BLOCKED>
 __global__ void __launch_bounds__(threads_of(TPR)) silu_mul_quantize_kernel(SiluArgs a) {
@@ -33,15 +47,8 @@ __global__ void __launch_bounds__(threads_of(TPR)) silu_mul_quantize_kernel(Silu
   for (int64_t row = (int64_t)blockIdx.x * kTeams + threadIdx.x / TPR; row < a.rows;
        row += (int64_t)gridDim.x * kTeams) {
     u32x4 rg[NV], ru[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = i * TPR + lane;
-      rg[i] = ru[i] = u32x4{0, 0, 0, 0};
-      if (j < nvec) {
-        rg[i] = reinterpret_cast<const u32x4*>(a.H)[2 * row * nvec + j];
-        ru[i] = reinterpret_cast<const u32x4*>(a.H)[(2 * row + 1) * nvec + j];
-      }
-    }
+    if (a.stream) load_halves<true, TPR>(a, row, lane, rg, ru);
+    else load_halves<false, TPR>(a, row, lane, rg, ru);
     F8 act[NV];
     uint32_t most = 0;
 #pragma unroll
@@ -52,8 +59,8 @@ __global__ void __launch_bounds__(threads_of(TPR)) silu_mul_quantize_kernel(Silu
         const float ag = __uint_as_float(row16_reduce(mag_max(g, 0), MaxU()));
         const float au = __uint_as_float(row16_reduce(mag_max(u, 0), MaxU()));
         if (j < nvec) {
-          reinterpret_cast<u32x2*>(a.HQ)[2 * row * nvec + j] = codes_of(g, inverse_scale(ag));
-          reinterpret_cast<u32x2*>(a.HQ)[(2 * row + 1) * nvec + j] = codes_of(u, inverse_scale(au));
+          store_out(reinterpret_cast<u32x2*>(a.HQ) + 2 * row * nvec + j, codes_of(g, inverse_scale(ag)));
+          store_out(reinterpret_cast<u32x2*>(a.HQ) + (2 * row + 1) * nvec + j, codes_of(u, inverse_scale(au)));
           if ((lane & 15) == 0) {
             a.h_scale[2 * row * nblocks + j / 16] = scale_of(ag);
             a.h_scale[(2 * row + 1) * nblocks + j / 16] = scale_of(au);
@@ -65,7 +72,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) silu_mul_quantize_kernel(Silu
       if constexpr (BLOCKED) {
         const float amax = __uint_as_float(row16_reduce(mag_max(act[i], 0), MaxU()));
         if (j < nvec) {
-          reinterpret_cast<u32x2*>(a.AQ)[row * nvec + j] = codes_of(act[i], inverse_scale(amax));
+          store_out(reinterpret_cast<u32x2*>(a.AQ) + row * nvec + j, codes_of(act[i], inverse_scale(amax)));
           if ((lane & 15) == 0) a.a_scale[row * nblocks + j / 16] = scale_of(amax);
         }
       } else {
@@ -85,7 +92,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) silu_mul_quantize_kernel(Silu
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int j = i * TPR + lane;
-        if (j < nvec) reinterpret_cast<u32x2*>(a.AQ)[row * nvec + j] = codes_of(act[i], inv);
+        if (j < nvec) store_out(reinterpret_cast<u32x2*>(a.AQ) + row * nvec + j, codes_of(act[i], inv));
       }
       if (lane == 0) a.a_scale[row] = scale_of(amax);
     }
@@ -115,8 +122,8 @@ __global__ void __launch_bounds__(256) silu_mul_backward_kernel(SiluBackwardArgs
       // sig (1 + g (1 - sig)) = sig + silu (1 - sig)
       dg.v[e] = da.v[e] * (qu.v[e] * su) * __builtin_fmaf(silu, 1.0f - s, s);
     }
-    reinterpret_cast<u32x4*>(a.dH)[2 * row * nvec + j] = pack_bf16(dg);
-    reinterpret_cast<u32x4*>(a.dH)[(2 * row + 1) * nvec + j] = pack_bf16(du);
+    store_out(reinterpret_cast<u32x4*>(a.dH) + 2 * row * nvec + j, pack_bf16(dg));
+    store_out(reinterpret_cast<u32x4*>(a.dH) + (2 * row + 1) * nvec + j, pack_bf16(du));
   }
 }
 
@@ -235,47 +242,43 @@ __device__ __forceinline__ void values(const Raw<E4M3>& r, float (&v)[E4M3 ? 16 
   }
 }
 
-// partial[c][k]: largest magnitude of column k in chunk c.  512 columns per workgroup;
-// its rows of lanes take every 4th (bf16) or 8th (codes) row.
+// partial[c][k]: largest magnitude of column k in chunk c.  The workgroups have the
+// tiles of the second kernel, in the same order: what one reads here its XCD's L2 may
+// still hold there (tiles of 512 columns: 9.0 + 13.5 us for the two kernels at 4096 x
+// 7168 codes, of 128: 9.5 + 11.7).
 template <bool E4M3>
 __global__ void __launch_bounds__(256) column_amax_kernel(KOffsetsArgs a, int tiles) {
   constexpr int W = E4M3 ? 16 : 8;
-  constexpr int kLanes = 512 / W, kRows = 256 / kLanes;
-  __shared__ uint32_t most[kRows][512 + 4];
-  const int chunk = blockIdx.x / tiles, col0 = (int)(blockIdx.x % tiles) * 512;
+  constexpr int kLanes = kTile / W, kRowLanes = 256 / kLanes, kRows = kChunkRows / kRowLanes;
+  __shared__ uint32_t most[kRowLanes][kTile + 4];
+  const int chunk = blockIdx.x / tiles, col0 = (int)(blockIdx.x % tiles) * kTile;
   const KChunk f = find_chunk(a, chunk);
   if (col0 == 0 && threadIdx.x == 0) a.table[chunk] = f;
   if (f.group < 0) return;
   const int lx = threadIdx.x % kLanes, ly = threadIdx.x / kLanes;
   const int col = col0 + lx * W;
+  Raw<E4M3> raw[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    raw[i] = Raw<E4M3>{{0, 0, 0, 0}, 0.f};
+    if (ly + i * kRowLanes < f.rows && col < a.K) raw[i] = load_raw<E4M3>(a, f.row + ly + i * kRowLanes, col);
+  }
   uint32_t m[W] = {};
-  if (col < a.K) {
-    // eight rows in flight
-    for (int r = ly; r < f.rows; r += 8 * kRows) {
-      Raw<E4M3> raw[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        raw[i] = Raw<E4M3>{{0, 0, 0, 0}, 0.f};
-        if (r + i * kRows < f.rows) raw[i] = load_raw<E4M3>(a, f.row + r + i * kRows, col);
-      }
+  for (int i = 0; i < kRows; ++i) {
+    float v[W];
+    values<E4M3>(raw[i], v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v[W];
-        values<E4M3>(raw[i], v);
-#pragma unroll
-        for (int e = 0; e < W; ++e) m[e] = umax(m[e], mag(v[e]));
-      }
-    }
+    for (int e = 0; e < W; ++e) m[e] = umax(m[e], mag(v[e]));
   }
 #pragma unroll
   for (int e = 0; e < W; ++e) most[ly][lx * W + e] = m[e];
   __syncthreads();
-  for (int x = threadIdx.x; x < 512; x += 256) {
-    if (col0 + x >= a.K) break;
-    uint32_t top = most[0][x];
+  if (threadIdx.x < kTile && col0 + (int)threadIdx.x < a.K) {
+    uint32_t top = most[0][threadIdx.x];
 #pragma unroll
-    for (int y = 1; y < kRows; ++y) top = umax(top, most[y][x]);
-    a.partial[(int64_t)chunk * a.K + col0 + x] = __uint_as_float(top);
+    for (int y = 1; y < kRowLanes; ++y) top = umax(top, most[y][threadIdx.x]);
+    a.partial[(int64_t)chunk * a.K + col0 + threadIdx.x] = __uint_as_float(top);
   }
 }
 
@@ -355,6 +358,8 @@ __global__ void __launch_bounds__(256) transpose_quantize_kernel(KOffsetsArgs a,
     const int k = i / 8, s = i % 8;
     if (col0 + k < a.K && s < runs) {
       const uint32_t* w = turned + k * kLdsStride + s * 4;
+      // through the caches: a run of 128 bytes starts anywhere, and the workgroups beside
+      // this one write the rest of its lines (13.5 against 21.8 us past the caches)
       *reinterpret_cast<u32x4*>(a.XT + (col0 + k) * a.cap + f.col + s * 16) = u32x4{w[0], w[1], w[2], w[3]};
     }
   }
@@ -382,13 +387,12 @@ hipError_t launch_silu_back(const SiluBackwardArgs& a, hipStream_t stream) {
 template <bool E4M3>
 hipError_t launch_k_offsets(const KOffsetsArgs& a, hipStream_t stream) {
   const int chunks = (int)k_offsets_chunks(a.R, a.G);
+  const int tiles = (a.K + kTile - 1) / kTile;
   if (chunks > 0) {
-    const int tiles = (a.K + 511) / 512;
     hipLaunchKernelGGL((column_amax_kernel<E4M3>), dim3(chunks * tiles), dim3(256), 0, stream, a, tiles);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int tiles = (a.K + kTile - 1) / kTile;
   hipLaunchKernelGGL((transpose_quantize_kernel<E4M3>), dim3((chunks + 1) * tiles), dim3(256), 0, stream, a, tiles,
                      chunks);
   return hipGetLastError();
@@ -396,8 +400,10 @@ hipError_t launch_k_offsets(const KOffsetsArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_silu_mul_quantize(const SiluArgs& a, int block, hipStream_t stream) {
+hipError_t launch_silu_mul_quantize(const SiluArgs& given, int block, hipStream_t stream) {
+  SiluArgs a = given;
   if (a.rows == 0) return hipSuccess;
+  a.stream = a.rows * a.I * 4 > kStreamBytes;
   const int nvec = a.I / 8;
   if (nvec <= 64) return launch_silu<64, 1>(a, block, stream);
   if (nvec <= 256) return launch_silu<256, 1>(a, block, stream);

@@ -157,7 +157,7 @@ fp8gg_status f8f8bf16_rmsnorm_quantize(const uint16_t* X, const uint16_t* residu
                    {"rstd", rstd, 4 * rows, 4, true, true}},
                   {{"residual", "residual_out"}}));
   const fp8gg::NormArgs a{X, residual, weight, XQ, x_scale, Y, residual_out, rstd, rows, (int32_t)K,
-                          weight_dtype == FP8GG_DTYPE_F32, eps};
+                          weight_dtype == FP8GG_DTYPE_F32, eps, 0};
   return launched(fp8gg::launch_rmsnorm_quantize(a, block, static_cast<hipStream_t>(stream)), "rmsnorm_quantize");
 }
 
@@ -322,7 +322,7 @@ fp8gg_status f8f8bf16_silu_mul_quantize(const uint16_t* H, int block, uint8_t* A
                    {"a_scale", a_scale, 4 * (block ? rows * (I / 128) : rows), 4, true, false},
                    {"HQ", HQ, 2 * n, 8, true, true},
                    {"h_scale", h_scale, 8 * rows * ((I + 127) / 128), 4, true, true}}));
-  const fp8gg::SiluArgs a{H, AQ, a_scale, HQ, h_scale, rows, (int32_t)I};
+  const fp8gg::SiluArgs a{H, AQ, a_scale, HQ, h_scale, rows, (int32_t)I, 0};
   return launched(fp8gg::launch_silu_mul_quantize(a, block, static_cast<hipStream_t>(stream)), "silu_mul_quantize");
 }
 

@@ -14,7 +14,8 @@
 // Backward.  Each team of threads walks rows team, team + parts, ...: one pass gathers
 // mean(w dY xhat), the row (still in registers) gives dX, and every thread keeps the
 // sum of dY xhat of its own columns in fp32 over all its rows.  The teams' sums go to
-// the workspace and a second kernel adds them in a fixed order.
+// the workspace and a second kernel adds them in a fixed order.  Loads past the caches
+// do not help here (55.2 against 54.1 us at 4093 x 7184).
 #include "fp8gg_layer_internal.h"
 
 namespace fp8gg {
@@ -64,6 +65,20 @@ __device__ __forceinline__ void team_reduce(float& sum, uint32_t& most, int slot
   }
 }
 
+template <bool STREAM, int TPR, int NV>
+__device__ __forceinline__ void load_row(const NormArgs& a, int64_t base, int lane, u32x4 (&raw)[NV], u32x4 (&res)[NV]) {
+  const int nvec = a.K / 8;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = i * TPR + lane;
+    raw[i] = res[i] = u32x4{0, 0, 0, 0};
+    if (j < nvec) {
+      raw[i] = load_in<STREAM>(reinterpret_cast<const u32x4*>(a.X) + base + j);
+      if (a.residual) res[i] = load_in<STREAM>(reinterpret_cast<const u32x4*>(a.residual) + base + j);
+    }
+  }
+}
+
 template <int TPR, int NV, bool BLOCKED>
 __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_quantize_kernel(NormArgs a) {
   constexpr int kTeams = threads_of(TPR) / TPR;
@@ -75,15 +90,8 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_quantize_kernel(NormA
   for (int64_t row = (int64_t)blockIdx.x * kTeams + team; row < a.rows; row += (int64_t)gridDim.x * kTeams) {
     const int64_t base = row * nvec;
     u32x4 raw[NV], res[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = i * TPR + lane;
-      raw[i] = res[i] = u32x4{0, 0, 0, 0};
-      if (j < nvec) {
-        raw[i] = reinterpret_cast<const u32x4*>(a.X)[base + j];
-        if (a.residual) res[i] = reinterpret_cast<const u32x4*>(a.residual)[base + j];
-      }
-    }
+    if (a.stream) load_row<true, TPR>(a, base, lane, raw, res);
+    else load_row<false, TPR>(a, base, lane, raw, res);
     F8 hw[NV];
     float sum = 0.f;
     uint32_t most = 0;
@@ -96,7 +104,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_quantize_kernel(NormA
 #pragma unroll
         for (int e = 0; e < 8; ++e) h.v[e] += r.v[e];
         const u32x4 rounded = pack_bf16(h);
-        if (j < nvec) reinterpret_cast<u32x4*>(a.residual_out)[base + j] = rounded;
+        if (j < nvec) store_out(reinterpret_cast<u32x4*>(a.residual_out) + base + j, rounded);
         h = unpack_bf16(rounded);
       }
       F8 w{};
@@ -114,7 +122,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_quantize_kernel(NormA
       for (int i = 0; i < NV; ++i) {
         const int j = i * TPR + lane;
         block_amax[i] = __uint_as_float(row16_reduce(mag_max(hw[i], 0), MaxU()));
-        if (j < nvec) reinterpret_cast<u32x2*>(a.XQ)[base + j] = codes_of(hw[i], inverse_scale(block_amax[i]));
+        if (j < nvec) store_out(reinterpret_cast<u32x2*>(a.XQ) + base + j, codes_of(hw[i], inverse_scale(block_amax[i])));
       }
     }
     team_reduce<TPR>(sum, most, slot);
@@ -133,7 +141,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_quantize_kernel(NormA
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int j = i * TPR + lane;
-        if (j < nvec) reinterpret_cast<u32x2*>(a.XQ)[base + j] = codes_of(hw[i], inv);
+        if (j < nvec) store_out(reinterpret_cast<u32x2*>(a.XQ) + base + j, codes_of(hw[i], inv));
       }
       if (lane == 0) a.x_scale[row] = amax == 0.f ? 1.f : rstd * scale_of(amax);
     }
@@ -144,67 +152,96 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_quantize_kernel(NormA
         F8 y;
 #pragma unroll
         for (int e = 0; e < 8; ++e) y.v[e] = hw[i].v[e] * rstd;
-        if (j < nvec) reinterpret_cast<u32x4*>(a.Y)[base + j] = pack_bf16(y);
+        if (j < nvec) store_out(reinterpret_cast<u32x4*>(a.Y) + base + j, pack_bf16(y));
       }
     }
     if (a.rstd && lane == 0) a.rstd[row] = rstd;
   }
 }
 
+// One row as it is loaded.
+template <int NV>
+struct BackRow {
+  u32x4 dy[NV], h[NV], dres[NV];
+  float rstd;
+};
+
+template <int TPR, int NV>
+__device__ __forceinline__ void load_back_row(const NormBackwardArgs& a, int64_t row, int lane, BackRow<NV>& r) {
+  const int nvec = a.K / 8;
+  const int64_t base = row * nvec;
+  r.rstd = a.rstd[row];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = i * TPR + lane;
+    r.dy[i] = r.h[i] = r.dres[i] = u32x4{0, 0, 0, 0};
+    if (j < nvec) {
+      r.dy[i] = reinterpret_cast<const u32x4*>(a.dY)[base + j];
+      r.h[i] = reinterpret_cast<const u32x4*>(a.H)[base + j];
+      if (a.dresidual) r.dres[i] = reinterpret_cast<const u32x4*>(a.dresidual)[base + j];
+    }
+  }
+}
+
+// With one vector per thread there are registers for the weights and for the next row,
+// which is asked for before this one is reduced (1024 threads and 256 teams against 256
+// threads, four vectors and 512 teams without: 54.4 -> 51.8 us at 4093 x 7184).
 template <int TPR, int NV>
 __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_backward_kernel(NormBackwardArgs a) {
+  constexpr bool kAhead = NV == 1;
   constexpr int kTeams = threads_of(TPR) / TPR;
   const int lane = threadIdx.x % TPR;
   const int team = blockIdx.x * kTeams + threadIdx.x / TPR;
   if (team >= a.parts) return;   // whole waves; teams of several waves fill their workgroup
   const int nvec = a.K / 8;
   const float inv_k = 1.0f / (float)a.K;
-  F8 dw[NV] = {};
+  F8 held[kAhead ? NV : 1], dw[NV] = {};
+  const auto weight = [&](int i) {
+    F8 w = {};
+    if (i * TPR + lane < nvec) w = load_weight(a.weight, a.w_f32, i * TPR + lane);
+    return w;
+  };
+  BackRow<NV> now, next;
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) held[i] = weight(i);
+    load_back_row<TPR, NV>(a, team, lane, now);
+  }
   int slot = 0;
   for (int64_t row = team; row < a.rows; row += a.parts) {
-    const int64_t base = row * nvec;
-    const float rstd = a.rstd[row];
-    u32x4 rdy[NV], rh[NV], rres[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = i * TPR + lane;
-      rdy[i] = rh[i] = rres[i] = u32x4{0, 0, 0, 0};
-      if (j < nvec) {
-        rdy[i] = reinterpret_cast<const u32x4*>(a.dY)[base + j];
-        rh[i] = reinterpret_cast<const u32x4*>(a.H)[base + j];
-        if (a.dresidual) rres[i] = reinterpret_cast<const u32x4*>(a.dresidual)[base + j];
-      }
-    }
+    if constexpr (!kAhead) load_back_row<TPR, NV>(a, row, lane, now);
+    else if (row + a.parts < a.rows) load_back_row<TPR, NV>(a, row + a.parts, lane, next);
     float dot = 0.f;
-    F8 wdy[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int j = i * TPR + lane;
-      const F8 dy = unpack_bf16(rdy[i]), h = unpack_bf16(rh[i]);
-      F8 w{};
-      if (j < nvec) w = load_weight(a.weight, a.w_f32, j);
+      F8 w;
+      if constexpr (kAhead) w = held[i];
+      else w = weight(i);
+      const F8 dy = unpack_bf16(now.dy[i]), h = unpack_bf16(now.h[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float xhat = h.v[e] * rstd;
-        wdy[i].v[e] = w.v[e] * dy.v[e];
-        dot = __builtin_fmaf(wdy[i].v[e], xhat, dot);
-        dw[i].v[e] = __builtin_fmaf(dy.v[e], xhat, dw[i].v[e]);
+        const float g = dy.v[e] * (h.v[e] * now.rstd);
+        dot = __builtin_fmaf(w.v[e], g, dot);
+        dw[i].v[e] += g;
       }
     }
     uint32_t unused = 0;
     team_reduce<TPR>(dot, unused, slot);
     slot ^= 1;
-    const float c = dot * inv_k * rstd;   // times h: xhat * mean(w dY xhat)
+    const float c = dot * inv_k * now.rstd;   // times h: xhat * mean(w dY xhat)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = i * TPR + lane;
-      const F8 h = unpack_bf16(rh[i]), dr = unpack_bf16(rres[i]);
-      F8 dx;
+      const F8 dy = unpack_bf16(now.dy[i]), h = unpack_bf16(now.h[i]), dr = unpack_bf16(now.dres[i]);
+      F8 w, dx;
+      if constexpr (kAhead) w = held[i];
+      else w = weight(i);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        dx.v[e] = __builtin_fmaf(__builtin_fmaf(-h.v[e], c, wdy[i].v[e]), rstd, dr.v[e]);
-      if (j < nvec) reinterpret_cast<u32x4*>(a.dX)[base + j] = pack_bf16(dx);
+        dx.v[e] = __builtin_fmaf(__builtin_fmaf(-h.v[e], c, w.v[e] * dy.v[e]), now.rstd, dr.v[e]);
+      if (j < nvec) store_out(reinterpret_cast<u32x4*>(a.dX) + row * nvec + j, pack_bf16(dx));
     }
+    if constexpr (kAhead) now = next;
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -262,19 +299,26 @@ hipError_t launch_back(const NormBackwardArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_rmsnorm_quantize(const NormArgs& a, int block, hipStream_t stream) {
+hipError_t launch_rmsnorm_quantize(const NormArgs& given, int block, hipStream_t stream) {
+  NormArgs a = given;
   if (a.rows == 0) return hipSuccess;
+  a.stream = a.rows * a.K * (a.residual ? 4 : 2) > kStreamBytes;
   const int nvec = a.K / 8;
   if (nvec <= 64) return launch_norm<64, 1>(a, block, stream);
   if (nvec <= 256) return launch_norm<256, 1>(a, block, stream);
   if (nvec <= 512) return launch_norm<256, 2>(a, block, stream);
-  if (nvec <= 1024) return launch_norm<256, 4>(a, block, stream);
+  // Row scales on two vectors per thread (16384 x 7168: 169.6 us against 173.3 on four; 8
+  // rows 3.2 against 4.0), block scales, which need no barrier before their codes, on
+  // four (177.8 against 183.1; 8 rows 4.0 against 3.2).  Not by the number of rows: a
+  // row's sums then come out the same in every batch.
+  if (nvec <= 1024) return block ? launch_norm<256, 4>(a, block, stream) : launch_norm<512, 2>(a, block, stream);
   return launch_norm<1024, 4>(a, block, stream);
 }
 
+// One workgroup per compute unit of 1024 threads, two of 512, and so on.
 int norm_backward_parts(int64_t rows, int64_t K) {
-  (void)K;
-  return (int)(rows < 512 ? rows : 512);
+  const int64_t nvec = K / 8, teams = nvec <= 64 ? 1024 : (nvec <= 512 ? 512 : 256);
+  return (int)(rows < teams ? rows : teams);
 }
 
 hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream) {
@@ -283,8 +327,9 @@ hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream
   if (a.rows > 0) {
     if (nvec <= 64) e = launch_back<64, 1>(a, stream);
     else if (nvec <= 256) e = launch_back<256, 1>(a, stream);
-    else if (nvec <= 512) e = launch_back<256, 2>(a, stream);
-    else if (nvec <= 1024) e = launch_back<256, 4>(a, stream);
+    else if (nvec <= 512) e = launch_back<512, 1>(a, stream);
+    else if (nvec <= 1024) e = launch_back<1024, 1>(a, stream);
+    else if (nvec <= 2048) e = launch_back<1024, 2>(a, stream);
     else e = launch_back<1024, 4>(a, stream);
   }
   if (e != hipSuccess) return e;
