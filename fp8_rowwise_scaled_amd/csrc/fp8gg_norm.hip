@@ -159,68 +159,76 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_quantize_kernel(NormA
   }
 }
 
-// One row as it is loaded.
-template <int NV>
-struct BackRow {
-  u32x4 dy[NV], h[NV], dres[NV];
-  float rstd;
+// Eight columns of one row as they are loaded.
+struct BackVec {
+  u32x4 dy, h, dres;
 };
 
-template <int TPR, int NV>
-__device__ __forceinline__ void load_back_row(const NormBackwardArgs& a, int64_t row, int lane, BackRow<NV>& r) {
+__device__ __forceinline__ BackVec load_back(const NormBackwardArgs& a, int64_t row, int j) {
   const int nvec = a.K / 8;
-  const int64_t base = row * nvec;
-  r.rstd = a.rstd[row];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int j = i * TPR + lane;
-    r.dy[i] = r.h[i] = r.dres[i] = u32x4{0, 0, 0, 0};
-    if (j < nvec) {
-      r.dy[i] = reinterpret_cast<const u32x4*>(a.dY)[base + j];
-      r.h[i] = reinterpret_cast<const u32x4*>(a.H)[base + j];
-      if (a.dresidual) r.dres[i] = reinterpret_cast<const u32x4*>(a.dresidual)[base + j];
-    }
+  BackVec v{{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+  if (j < nvec) {
+    v.dy = reinterpret_cast<const u32x4*>(a.dY)[row * nvec + j];
+    v.h = reinterpret_cast<const u32x4*>(a.H)[row * nvec + j];
+    if (a.dresidual) v.dres = reinterpret_cast<const u32x4*>(a.dresidual)[row * nvec + j];
   }
+  return v;
 }
 
-// With one vector per thread there are registers for the weights and for the next row,
-// which is asked for before this one is reduced (1024 threads and 256 teams against 256
-// threads, four vectors and 512 teams without: 54.4 -> 51.8 us at 4093 x 7184).
+// What a thread keeps depends on the registers that its columns leave.  One vector (or two
+// in small workgroups): the weights, and the next row, which is asked for before this one
+// is reduced (1024 threads and 256 teams so, against 256 threads, four vectors and 512
+// teams without: 54.4 -> 51.8 us at 4093 x 7184).  Two vectors of 1024 threads: the row.
+// Four: nothing, the second pass over the row reads it again (kept, it went through
+// scratch memory: 130 us at 1228 x 20480).
 template <int TPR, int NV>
 __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_backward_kernel(NormBackwardArgs a) {
-  constexpr bool kAhead = NV == 1;
   constexpr int kTeams = threads_of(TPR) / TPR;
+  constexpr bool kAhead = NV == 1 || TPR == 64;
+  constexpr bool kKept = NV <= 2;
   const int lane = threadIdx.x % TPR;
   const int team = blockIdx.x * kTeams + threadIdx.x / TPR;
   if (team >= a.parts) return;   // whole waves; teams of several waves fill their workgroup
   const int nvec = a.K / 8;
   const float inv_k = 1.0f / (float)a.K;
   F8 held[kAhead ? NV : 1], dw[NV] = {};
+  BackVec now[kKept ? NV : 1], next[kAhead ? NV : 1];
   const auto weight = [&](int i) {
     F8 w = {};
-    if (i * TPR + lane < nvec) w = load_weight(a.weight, a.w_f32, i * TPR + lane);
+    if constexpr (kAhead) w = held[i];
+    else if (i * TPR + lane < nvec) w = load_weight(a.weight, a.w_f32, i * TPR + lane);
     return w;
   };
-  BackRow<NV> now, next;
+  const auto vec = [&](int64_t row, int i) {
+    if constexpr (kKept) return now[i];
+    else return load_back(a, row, i * TPR + lane);
+  };
   if constexpr (kAhead) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) held[i] = weight(i);
-    load_back_row<TPR, NV>(a, team, lane, now);
+    for (int i = 0; i < NV; ++i) {
+      held[i] = F8{};
+      if (i * TPR + lane < nvec) held[i] = load_weight(a.weight, a.w_f32, i * TPR + lane);
+      now[i] = load_back(a, team, i * TPR + lane);
+    }
   }
   int slot = 0;
   for (int64_t row = team; row < a.rows; row += a.parts) {
-    if constexpr (!kAhead) load_back_row<TPR, NV>(a, row, lane, now);
-    else if (row + a.parts < a.rows) load_back_row<TPR, NV>(a, row + a.parts, lane, next);
+    const float rstd = a.rstd[row];
+    if constexpr (kKept) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if constexpr (!kAhead) now[i] = load_back(a, row, i * TPR + lane);
+        else if (row + a.parts < a.rows) next[i] = load_back(a, row + a.parts, i * TPR + lane);
+      }
+    }
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      F8 w;
-      if constexpr (kAhead) w = held[i];
-      else w = weight(i);
-      const F8 dy = unpack_bf16(now.dy[i]), h = unpack_bf16(now.h[i]);
+      const BackVec v = vec(row, i);
+      const F8 w = weight(i), dy = unpack_bf16(v.dy), h = unpack_bf16(v.h);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float g = dy.v[e] * (h.v[e] * now.rstd);
+        const float g = dy.v[e] * (h.v[e] * rstd);
         dot = __builtin_fmaf(w.v[e], g, dot);
         dw[i].v[e] += g;
       }
@@ -228,20 +236,22 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_backward_kernel(NormB
     uint32_t unused = 0;
     team_reduce<TPR>(dot, unused, slot);
     slot ^= 1;
-    const float c = dot * inv_k * now.rstd;   // times h: xhat * mean(w dY xhat)
+    const float c = dot * inv_k * rstd;   // times h: xhat * mean(w dY xhat)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = i * TPR + lane;
-      const F8 dy = unpack_bf16(now.dy[i]), h = unpack_bf16(now.h[i]), dr = unpack_bf16(now.dres[i]);
-      F8 w, dx;
-      if constexpr (kAhead) w = held[i];
-      else w = weight(i);
+      const BackVec v = vec(row, i);
+      const F8 w = weight(i), dy = unpack_bf16(v.dy), h = unpack_bf16(v.h), dr = unpack_bf16(v.dres);
+      F8 dx;
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        dx.v[e] = __builtin_fmaf(__builtin_fmaf(-h.v[e], c, w.v[e] * dy.v[e]), now.rstd, dr.v[e]);
+        dx.v[e] = __builtin_fmaf(__builtin_fmaf(-h.v[e], c, w.v[e] * dy.v[e]), rstd, dr.v[e]);
       if (j < nvec) store_out(reinterpret_cast<u32x4*>(a.dX) + row * nvec + j, pack_bf16(dx));
     }
-    if constexpr (kAhead) now = next;
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) now[i] = next[i];
+    }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -303,21 +313,29 @@ hipError_t launch_rmsnorm_quantize(const NormArgs& given, int block, hipStream_t
   NormArgs a = given;
   if (a.rows == 0) return hipSuccess;
   a.stream = a.rows * a.K * (a.residual ? 4 : 2) > kStreamBytes;
+  // Threads and vectors per row, by K alone (a row's sums then come out the same in every
+  // batch).  Measured with 24 M elements, us: K = 512: a wave per row 32.5, 256 threads
+  // 61.5.  2048: 256 threads 31.2, a wave with four vectors 31.7 (16 rows: 3.0 and 4.0).
+  // 4096: 512 threads 30.1, 256 with two vectors 31.2.  7168, row scales: 512 with two
+  // 30.8, 256 with four 32.9, 1024 with one 32.2; block scales, which need no barrier
+  // before their codes: 35.3, 34.3, 33.8, and at 16384 rows 183, 178, 187.  16384: 1024
+  // with two 32.4, 512 with four 33.2, 1024 with four 41.3.
   const int nvec = a.K / 8;
   if (nvec <= 64) return launch_norm<64, 1>(a, block, stream);
+  if (nvec <= 128) return launch_norm<64, 2>(a, block, stream);
   if (nvec <= 256) return launch_norm<256, 1>(a, block, stream);
-  if (nvec <= 512) return launch_norm<256, 2>(a, block, stream);
-  // Row scales on two vectors per thread (16384 x 7168: 169.6 us against 173.3 on four; 8
-  // rows 3.2 against 4.0), block scales, which need no barrier before their codes, on
-  // four (177.8 against 183.1; 8 rows 4.0 against 3.2).  Not by the number of rows: a
-  // row's sums then come out the same in every batch.
+  if (nvec <= 512) return launch_norm<512, 1>(a, block, stream);
   if (nvec <= 1024) return block ? launch_norm<256, 4>(a, block, stream) : launch_norm<512, 2>(a, block, stream);
+  if (nvec <= 2048) return launch_norm<1024, 2>(a, block, stream);
   return launch_norm<1024, 4>(a, block, stream);
 }
 
-// One workgroup per compute unit of 1024 threads, two of 512, and so on.
+// One workgroup per compute unit of 1024 threads, two of 256 or 512; 2048 teams of one
+// wave (K = 512, 24 M elements: 37.5 us, 1024 teams 49.8, 4096 40.6, 512 of 256 threads
+// 101).  More teams read and write more partial sums (K = 2048: 512 teams 38.6, 1024
+// 40.3, 256 59.8).
 int norm_backward_parts(int64_t rows, int64_t K) {
-  const int64_t nvec = K / 8, teams = nvec <= 64 ? 1024 : (nvec <= 512 ? 512 : 256);
+  const int64_t nvec = K / 8, teams = nvec <= 128 ? 2048 : (nvec <= 512 ? 512 : 256);
   return (int)(rows < teams ? rows : teams);
 }
 
@@ -325,7 +343,10 @@ hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream
   const int nvec = a.K / 8;
   hipError_t e = hipSuccess;
   if (a.rows > 0) {
+    // as for the forward pass; 4096: 512 threads 39.8 us, 256 with two vectors 43.1; 7168:
+    // 1024 with one 39.9, 512 with two 44.2; 12288: 1024 with two 45.8, 512 with four 48.7
     if (nvec <= 64) e = launch_back<64, 1>(a, stream);
+    else if (nvec <= 128) e = launch_back<64, 2>(a, stream);
     else if (nvec <= 256) e = launch_back<256, 1>(a, stream);
     else if (nvec <= 512) e = launch_back<512, 1>(a, stream);
     else if (nvec <= 1024) e = launch_back<1024, 1>(a, stream);

@@ -34,7 +34,7 @@ def hidden(rng, rows, I):
 
 
 CASES = [(1, 8), (5, 120), (4, 128), (6, 136), (9, 512), (7, 520), (130, 1000), (33, 2048), (5, 2056), (6, 4096), (4, 5000), (3, 8192),
-         (2, 8200), (2, 14336), (1, 32768), (300, 256)]
+         (2, 8200), (2, 14336), (1, 32768), (300, 256), (3, 1024), (2, 1032), (2, 16392)]
 
 
 @pytest.mark.parametrize("rows,I", CASES)

@@ -34,7 +34,8 @@ def rows_of(rng, rows, K, special=True):
 
 
 CASES = [(1, 8), (3, 16), (5, 504), (4, 512), (7, 520), (130, 1024), (33, 2048), (9, 2056), (6, 4096), (5, 4104),
-         (17, 7168), (4, 7184), (3, 8192), (2, 8200), (5, 12288), (2, 32768), (300, 256), (1, 7168)]
+         (17, 7168), (4, 7184), (3, 8192), (2, 8200), (5, 12288), (2, 32768), (300, 256), (1, 7168), (3, 1032), (2, 16384),
+         (3, 16392)]
 
 
 @pytest.mark.parametrize("rows,K", CASES)
@@ -132,10 +133,11 @@ def test_backward(F, rows, K, residual):
     P.assert_close(dw.t, want_w, (rows + 48) * P.U * np.abs(DY * xhat).sum(0) + 1e-30, "dweight")
 
 
-def test_backward_in_place_and_no_rows(F):
+@pytest.mark.parametrize("K", [264, 776, 1032, 5000, 7168, 12288, 20480])
+def test_backward_in_place_and_no_rows(F, K):
     rng = np.random.default_rng(9)
-    h, dy, dres = (rows_of(rng, 40, 776) for _ in range(3))
-    w, rstd = torch.ones(776, device="cuda"), torch.rand(40, device="cuda") + 0.5
+    h, dy, dres = (rows_of(rng, 40, K) for _ in range(3))
+    w, rstd = torch.ones(K, device="cuda"), torch.rand(40, device="cuda") + 0.5
     dx, dw = F.f8f8bf16_rmsnorm_backward(dy.cuda(), h.cuda(), w, rstd, dres.cuda())
     a, b = dy.cuda(), dres.cuda()
     x1, w1 = F.f8f8bf16_rmsnorm_backward(a, h.cuda(), w, rstd, dres.cuda(), dX=a)
