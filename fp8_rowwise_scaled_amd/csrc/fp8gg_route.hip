@@ -1,8 +1,8 @@
 // Routing of tokens to experts, its plan (rows per expert, places of the pairs) and
 // its gradient (gfx950).
 //
-// Choice.  A team of 16 lanes (E <= 256; else the wave's 64) holds one token's keys in
-// registers, up to 16 per lane.  The k-th largest of 16 lanes' own maxima bounds the
+// Choice.  A team of 16 lanes (E <= 512; else the wave's 64) holds one token's keys in
+// registers, up to 32 per lane.  The k-th largest of 16 lanes' own maxima bounds the
 // k-th largest key from below; the keys that reach it, a dozen or so of 256, go to LDS,
 // and each of them finds its rank by comparing itself with the others.  That is about a
 // third of the instructions of k rounds of a maximum over the team (48 us at 16384
@@ -84,10 +84,10 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 // fp32 keys p + bias.  Their error, with u = 2^-24: the rounded exponent makes exp(x)
 // off by 2 u |x| relative to itself, exp2 and the reciprocal by 2 u each.  Sigmoid:
 // p (1 - p) |x| <= 0.23 and p (1 - p) <= 0.25, so p is off by at most 5 u and the key by
-// u more per unit of its size.  Softmax: p |x - max| <= 0.37, and the sum of E <= 1024
-// positive terms (16 per lane, then 6 steps) adds at most 22 u.  So a key is within 8 u
-// (sigmoid) or 32 u (softmax), and two sums of two keys are told apart by more than four
-// times that: 2^-19 and 2^-17.
+// u more per unit of its size.  Softmax: p |x - max| <= 0.37, and the sum of positive
+// terms (32 per lane, then 4 steps; or 16, then 6) adds at most 36 u.  So a key is within
+// 8 u (sigmoid) or 44 u (softmax), and two sums of two keys are told apart by more than
+// four times that: 2^-19 = 32 u and 2^-16 = 256 u cover both.
 template <int L, int V>
 __device__ __forceinline__ void make_keys(const RouteArgs& a, int l, const float (&x)[V], float (&key)[V]) {
   if (a.sigmoid) {
@@ -119,7 +119,7 @@ __device__ __forceinline__ void make_keys(const RouteArgs& a, int l, const float
 template <typename K>
 __device__ __forceinline__ K margin_of(const RouteArgs& a, K s) {
   const K size = s > K(1) ? s : (s < K(-1) ? -s : K(1));
-  return size * (a.sigmoid ? K(0x1p-19) : K(0x1p-17));
+  return size * (a.sigmoid ? K(0x1p-19) : K(0x1p-16));
 }
 
 // The key of one expert in fp64, from its logit in memory (taken seldom, so nothing is
@@ -715,7 +715,8 @@ hipError_t launch_by_width(const RouteArgs& a, int blocks, hipStream_t stream) {
   if (a.E <= 64) return launch<16, 4, ARITH>(a, blocks, stream);
   if (a.E <= 128) return launch<16, 8, ARITH>(a, blocks, stream);
   if (a.E <= 256) return launch<16, 16, ARITH>(a, blocks, stream);
-  if (a.E <= 512) return launch<64, 8, ARITH>(a, blocks, stream);
+  // 16384 tokens, k = 8, us: 384 experts on 16 lanes 27.0, on 64 lanes 39.9; 512: 25.2, 37.4
+  if (a.E <= 512) return launch<16, 32, ARITH>(a, blocks, stream);
   return launch<64, 16, ARITH>(a, blocks, stream);
 }
 
