@@ -445,39 +445,61 @@ __device__ __forceinline__ void rank_exactly(const RouteArgs& a, int l, int n, C
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
-// Places of the pairs of one workgroup's tokens.  base[e]: the place of the block's
-// first pair of expert e.  Every wave takes a run of 64-pair pieces: it counts them, and
-// ranks them from the counts of the waves before it.
+// Places of the pairs of one workgroup's tokens.  Every wave takes a run of 64-pair
+// pieces; it counts its pairs by expert and ranks them from the counts of the waves
+// before it.
+struct Pieces {
+  int n, first, end;   // pairs of the workgroup; the wave's pieces
+};
+__device__ __forceinline__ Pieces pieces_of(int n) {
+  const int pieces = (n + 63) / 64, per_wave = (pieces + kWaves - 1) / kWaves;
+  const int first = (int)(threadIdx.x >> 6) * per_wave;
+  return {n, first, first + per_wave < pieces ? first + per_wave : pieces};
+}
+
+// The expert of the lane's pair in piece p (-1: none), from memory.
 template <typename Ids>
-__device__ __forceinline__ void place_pairs(Ids ids, int n, int E, const int* base, int* counts, int32_t* dst) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int pieces = (n + 63) / 64;
-  const int per_wave = (pieces + kWaves - 1) / kWaves;
-  const int first = wave * per_wave, end = first + per_wave < pieces ? first + per_wave : pieces;
-  const int bits = 32 - __clz(E);                    // E itself marks a slot without an expert
-  int* own = counts + wave * E;
-  for (int i = threadIdx.x; i < kWaves * E; i += kThreads) counts[i] = 0;
-  __syncthreads();
-  for (int p = first; p < end; ++p) {
-    const int i = p * 64 + lane;
-    const int e = i < n ? ids(i) : -1;
+__device__ __forceinline__ int pair_of(const Pieces& w, int p, Ids ids) {
+  const int i = p * 64 + (threadIdx.x & 63);
+  return p < w.end && i < w.n ? ids(i) : -1;
+}
+
+// The first kHeld pieces' experts are held in registers (given), the others read again.
+constexpr int kHeld = 4;
+template <typename Ids>
+__device__ __forceinline__ void count_pairs(const Pieces& w, Ids ids, const int (&held)[kHeld], int* own) {
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (held[u] >= 0) atomicAdd(&own[held[u]], 1);
+  for (int p = w.first + kHeld; p < w.end; ++p) {
+    const int e = pair_of(w, p, ids);
     if (e >= 0) atomicAdd(&own[e], 1);
   }
-  __syncthreads();
+}
+
+// counts[wave][e]: from the number of pairs to the place of the first one; base[e]: the
+// place of the workgroup's first pair of expert e.
+__device__ __forceinline__ void start_places(int E, int base, int* counts) {
   if ((int)threadIdx.x < E) {
-    int c[kWaves], at = base[threadIdx.x];
+    int c[kWaves];
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) c[w] = counts[w * E + threadIdx.x];
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      counts[w * E + threadIdx.x] = at;
-      at += c[w];
+      counts[w * E + threadIdx.x] = base;
+      base += c[w];
     }
   }
   __syncthreads();
-  for (int p = first; p < end; ++p) {
+}
+
+template <typename Ids>
+__device__ __forceinline__ void place_pairs(const Pieces& w, Ids ids, const int (&held)[kHeld], int E, int* own,
+                                            int32_t* dst) {
+  const int lane = threadIdx.x & 63;
+  const int bits = 32 - __clz(E);                    // E itself marks a slot without an expert
+  const auto piece = [&](int p, int id) {
     const int i = p * 64 + lane;
-    const int id = i < n ? ids(i) : -1;
     const int e = id < 0 ? E : id;
     uint64_t same = ~uint64_t(0);
     for (int b = 0; b < bits; ++b) {
@@ -491,11 +513,15 @@ __device__ __forceinline__ void place_pairs(Ids ids, int n, int E, const int* ba
       dst[i] = at + before;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       if (before == 0) own[e] = at + __popcll(same);
-    } else if (i < n) {
+    } else if (i < w.n) {
       dst[i] = -1;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (w.first + u < w.end) piece(w.first + u, held[u]);
+  for (int p = w.first + kHeld; p < w.end; ++p) piece(p, pair_of(w, p, ids));
 }
 
 // Exclusive prefix sum over the workgroup's threads.
@@ -619,11 +645,17 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
   const int c = count[threadIdx.x];                // 0 beyond E
   const int before = prefix_before(c, wave_sums);
   if ((int)threadIdx.x < a.E) a.M_sizes[threadIdx.x] = c;
+  int* counts = reinterpret_cast<int*>(dynamic_lds);
+  int* own = counts + wave * a.E;
+  for (int i = threadIdx.x; i < kWaves * a.E; i += kThreads) counts[i] = 0;
   __syncthreads();
-  count[threadIdx.x] = before;
+  const Pieces w = pieces_of((int)a.T * a.k);      // at most one per wave
+  const auto ids = [&](int i) { return chosen[i]; };
+  const int held[kHeld] = {pair_of(w, w.first, ids), -1, -1, -1};
+  count_pairs(w, ids, held, own);
   __syncthreads();
-  place_pairs([&](int i) { return chosen[i]; }, (int)a.T * a.k, a.E, count, reinterpret_cast<int*>(dynamic_lds),
-              a.dst_row);
+  start_places(a.E, before, counts);
+  place_pairs(w, ids, held, a.E, own, a.dst_row);
 }
 
 // Second kernel of the plan: each workgroup takes the pairs of `span` neighbouring blocks
@@ -631,68 +663,79 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
 // then places its pairs.  At most 64 workgroups, because each of them reads all counts
 // (256 x 256 of them at 16384 tokens and 256 experts: one workgroup per block took 21 us).
 constexpr int kPlaceGroups = 64;
+
+// LDS of the second kernel: the waves' counts, and for each of the kThreads / width sets
+// of lanes that read the first kernel's counts side by side their two sums.
+__host__ __device__ inline int place_width(int E) {
+  const int lanes = E % 4 == 0 ? E / 4 : E;
+  int width = 64;
+  while (width < lanes) width *= 2;
+  return width;
+}
+inline size_t place_lds(int E) { return (size_t)(kWaves + 2 * (kThreads / place_width(E))) * E * sizeof(int); }
+
+// Sums of the counts of all blocks and of those before `first_block`; four experts per
+// lane where the rows allow 16-byte loads, sixteen loads in flight.
+template <typename V>
+__device__ __forceinline__ void add_counts(const V* hist, int row, int lanes, int width, int blocks, int first_block,
+                                           V* sums) {
+  const int lane = threadIdx.x % width, set = threadIdx.x / width, sets = kThreads / width;
+  if (lane >= lanes) return;
+  V all = {}, prior = {};
+  for (int b = set; b < blocks; b += 16 * sets) {
+    V c[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      c[i] = V{};
+      if (b + i * sets < blocks) c[i] = hist[(int64_t)(b + i * sets) * row + lane];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      all += c[i];
+      if (b + i * sets < first_block) prior += c[i];
+    }
+  }
+  sums[set * lanes + lane] = all;
+  sums[(sets + set) * lanes + lane] = prior;
+}
+
 __global__ void __launch_bounds__(kThreads) place_kernel(RouteArgs a, int blocks, int span) {
   extern __shared__ double dynamic_lds[];
-  __shared__ int total[kMaxExperts];
-  __shared__ int earlier[kMaxExperts];
   __shared__ int wave_sums[kWaves];
-  total[threadIdx.x] = 0;
-  earlier[threadIdx.x] = 0;
-  __syncthreads();
-  // lanes of experts side by side, as many rows of counts at once as fit; four experts
-  // per lane where the rows allow it
+  int* counts = reinterpret_cast<int*>(dynamic_lds);
+  int* own = counts + (threadIdx.x >> 6) * a.E;
+  int* sums = counts + kWaves * a.E;
   const int first_block = blockIdx.x * span;
-  const int lanes = a.E % 4 == 0 ? a.E / 4 : a.E;
-  int width = 1;
-  while (width < lanes) width *= 2;
-  const int step = kThreads / width;
-  const int e = threadIdx.x % width;
-  if (a.E % 4 == 0 && e < lanes) {
-    u32x4 all = {0, 0, 0, 0}, prior = {0, 0, 0, 0};
-    for (int b = threadIdx.x / width; b < blocks; b += 16 * step) {
-      u32x4 c[16];                                 // sixteen loads in flight
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        c[i] = u32x4{0, 0, 0, 0};
-        if (b + i * step < blocks) c[i] = reinterpret_cast<const u32x4*>(a.hist + (int64_t)(b + i * step) * a.E)[e];
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        all += c[i];
-        if (b + i * step < first_block) prior += c[i];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      atomicAdd(&total[4 * e + i], (int)all[i]);
-      atomicAdd(&earlier[4 * e + i], (int)prior[i]);
-    }
-  } else if (a.E % 4 != 0 && e < a.E) {
-    int all = 0, prior = 0;
-    for (int b = threadIdx.x / width; b < blocks; b += 16 * step) {
-      int c[16];                                   // sixteen loads in flight
-#pragma unroll
-      for (int i = 0; i < 16; ++i) c[i] = b + i * step < blocks ? a.hist[(int64_t)(b + i * step) * a.E + e] : 0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        all += c[i];
-        prior += b + i * step < first_block ? c[i] : 0;
-      }
-    }
-    atomicAdd(&total[e], all);
-    atomicAdd(&earlier[e], prior);
-  }
-  __syncthreads();
-  const int c = total[threadIdx.x];
-  const int before = prefix_before(c, wave_sums);
-  if (blockIdx.x == 0 && (int)threadIdx.x < a.E) a.M_sizes[threadIdx.x] = c;
-  earlier[threadIdx.x] += before;
-  __syncthreads();
   const int64_t first = (int64_t)first_block * a.block_tokens, most = (int64_t)span * a.block_tokens;
-  const int n = (int)(a.T - first < most ? a.T - first : most) * a.k;
-  const int32_t* ids = a.ids + first * a.k;
-  place_pairs([&](int i) { return ids[i]; }, n, a.E, earlier, reinterpret_cast<int*>(dynamic_lds),
-              a.dst_row + first * a.k);
+  const Pieces w = pieces_of((int)(a.T - first < most ? a.T - first : most) * a.k);
+  const int32_t* block_ids = a.ids + first * a.k;
+  const auto ids = [&](int i) { return block_ids[i]; };
+  // The pairs are asked for first, so that counting them does not wait for the counts.
+  int held[kHeld];
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) held[u] = pair_of(w, w.first + u, ids);
+  for (int i = threadIdx.x; i < kWaves * a.E; i += kThreads) counts[i] = 0;
+  __syncthreads();
+  const int width = place_width(a.E), sets = kThreads / width;
+  count_pairs(w, ids, held, own);
+  if (a.E % 4 == 0)
+    add_counts(reinterpret_cast<const u32x4*>(a.hist), a.E / 4, a.E / 4, width, blocks, first_block,
+               reinterpret_cast<u32x4*>(sums));
+  else
+    add_counts(reinterpret_cast<const uint32_t*>(a.hist), a.E, a.E, width, blocks, first_block,
+               reinterpret_cast<uint32_t*>(sums));
+  __syncthreads();
+  int total = 0, earlier = 0;
+  if ((int)threadIdx.x < a.E) {
+    for (int s = 0; s < sets; ++s) {
+      total += sums[s * a.E + threadIdx.x];
+      earlier += sums[(sets + s) * a.E + threadIdx.x];
+    }
+    if (blockIdx.x == 0) a.M_sizes[threadIdx.x] = total;
+  }
+  earlier += prefix_before(total, wave_sums);
+  start_places(a.E, earlier, counts);
+  place_pairs(w, ids, held, a.E, own, a.dst_row + first * a.k);
 }
 
 template <int L, int V, bool ARITH>
@@ -817,8 +860,8 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
   hipError_t e = arith ? launch_by_width<true>(a, blocks, stream) : launch_by_width<false>(a, blocks, stream);
   if (e != hipSuccess || !a.M_sizes || blocks == 1) return e;
   const int span = (blocks + kPlaceGroups - 1) / kPlaceGroups;
-  hipLaunchKernelGGL(place_kernel, dim3((blocks + span - 1) / span), dim3(kThreads), (size_t)kWaves * a.E * sizeof(int),
-                     stream, a, blocks, span);
+  hipLaunchKernelGGL(place_kernel, dim3((blocks + span - 1) / span), dim3(kThreads), place_lds(a.E), stream, a,
+                     blocks, span);
   return hipGetLastError();
 }
 

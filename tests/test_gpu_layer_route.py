@@ -133,11 +133,12 @@ def test_masks_and_infinities(F):
             check(F, t, 6, torch.from_numpy(b), n_group=8, topk_group=3, group_top=2, **kw)
 
 
-@pytest.mark.parametrize("T", [64, 65, 1000, 16384, 16385, 40000])
-def test_many_tokens(F, T):
-    """One to 256 workgroups of 64 tokens, then several passes per workgroup; compared
-    with a sort on the GPU, the oracle being slow here."""
-    E, k = 60, 4
+@pytest.mark.parametrize("T,E,k", [(64, 60, 4), (65, 60, 4), (1000, 60, 4), (16384, 60, 4), (16385, 60, 4), (40000, 60, 4),
+                                   (40000, 61, 9), (70000, 256, 16), (3000, 1000, 5)])
+def test_many_tokens(F, T, E, k):
+    """One to 256 workgroups of 64 tokens, then several passes per workgroup, and more
+    pairs per wave of the plan than its registers hold; compared with a sort on the GPU,
+    the oracle being slow here."""
     g = torch.Generator(device="cuda").manual_seed(T)
     x = torch.randn(T, E, generator=g, device="cuda")
     r = F.f8f8bf16_route(x, k)
