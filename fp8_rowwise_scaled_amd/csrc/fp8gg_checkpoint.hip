@@ -7,7 +7,8 @@
 // pass reads H once: a wave's 16 lanes x 8 columns are one scale block, so the block's
 // largest magnitude is a reduction over 16 lanes; the activation itself stays in
 // registers until the row's largest magnitude is known.  The backward pass is
-// elementwise.  All are bound by HBM.
+// elementwise.  Both are bound by HBM: 16384 x 2048 with the checkpoint 38.5 us, 6.2 TB/s;
+// backward, 5001 x 1000 7.8 us, 5.2 TB/s.
 #include "fp8gg_layer_internal.h"
 
 namespace fp8gg {
@@ -136,7 +137,10 @@ __global__ void __launch_bounds__(256) silu_mul_backward_kernel(SiluBackwardArgs
 // joins the chunks of the group, requantises its own 128 rows x 128 columns and turns
 // them through LDS, so that both sides are accessed in runs of at least 128 bytes.  The
 // rows are read twice; the second time the Infinity Cache holds them unless they pass
-// 256 MB.
+// 256 MB.  4096 x 7168 codes in 8 groups: 9.5 + 11.8 us, 20 in a loop.  One kernel whose
+// workgroups take a whole group's 128 columns, the rows kept in registers between the two
+// steps, reads them once but waits for its largest group: 25 us there, 91 against 27 in 64
+// groups, 46 against 21 in one.
 
 constexpr int kTile = 128;             // columns of the second kernel's tile
 constexpr int kLdsStride = 33;         // words per column: 128 codes and one of padding

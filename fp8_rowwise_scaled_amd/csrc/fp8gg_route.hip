@@ -19,6 +19,12 @@
 // tokens' experts, the second kernel adds up the counts before its own block and ranks
 // the block's pairs by comparing expert numbers within a wave (ballots over their bits)
 // and counting across waves.  Integer sums only, so the order is fixed.
+//
+// 16384 tokens, 256 experts in 8 groups, k = 8, sigmoid and bias: 18 us for the choice (15
+// alone in a loop), 8.5 for the plan.  The logits (16.8 MB) take 3.2 us at a copy's rate;
+// what bounds the choice is its 1300 vector instructions per four tokens, and at its end
+// the few tokens decided in fp64 (up to 4 us after the others).  16 tokens, 8 experts: one
+// launch, 4.7 us.
 #include "fp8gg_layer_internal.h"
 
 namespace fp8gg {

@@ -52,7 +52,8 @@ typedef enum {
 } fp8gg_score;
 
 /*
- * Root-mean-square norm with the residual's addition and an fp8 output:
+ * Root-mean-square norm with the residual's addition and an fp8 output (the scale's floor
+ * is applied to h * weight, before rstd; h^2 has to be finite in fp32):
  *
  *     h    = bf16_rne(X + residual)          (h = X without a residual)
  *     rstd = 1 / sqrt(mean_k h^2 + eps)
