@@ -178,13 +178,10 @@ struct GroupOf {
 
 constexpr int kMaxGroups = 16;
 
-// The groups kept, as a mask, from lane g's (g < n_group) score, its rank and its distance
-// to the nearest score ahead of it.  `near`: the first group dropped is too close to the
-// last one kept for fp32.
+// The groups kept, as a mask, from lane g's (g < n_group) score and its rank.
 template <typename K, int L>
-__device__ __forceinline__ uint32_t groups_within(const RouteArgs& a, int l, int tok, K s, int rank, K gap, bool& near) {
+__device__ __forceinline__ uint32_t groups_within(const RouteArgs& a, int l, int tok, K s, int rank) {
   const bool real = l < a.n_group && s > none<K>();
-  near = real && rank == a.topk_group && gap <= margin_of(a, s + gap);
   return (uint32_t)(__ballot(real && rank < a.topk_group) >> (L == 64 ? 0 : tok * L)) & 0xFFFFu;
 }
 
@@ -227,8 +224,7 @@ __device__ __forceinline__ uint32_t keep_groups_exactly(const RouteArgs& a, int 
     const double other = __shfl(m1, (L == 64 ? 0 : tok * L) + o, 64);
     rank += other > m1 || (other == m1 && o < l);
   }
-  bool near;
-  return groups_within<double, L>(a, l, tok, m1, rank, 0.0, near);
+  return groups_within<double, L>(a, l, tok, m1, rank);
 }
 
 // The groups kept, by way of the token's own LDS: kMaxGroups best and second keys and E +
@@ -267,6 +263,12 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int64_t t, i
     take(o1);
     m2 = o2 > m2 ? o2 : m2;
   }
+  // A sum may be far smaller than what was added: its error goes by the largest key.
+  float largest = 0.f;
+  if (ARITH && g < a.n_group) {
+    if (m1 > none<float>()) largest = fabsf(m1);
+    if (m2 > none<float>()) largest = MaxK()(largest, fabsf(m2));
+  }
   if (g < a.n_group) {
     best[g] = a.group_top == 2 && m2 > none<float>() ? m1 + m2 : m1;
     second[g] = a.group_top == 2 && m2 > none<float>() ? m2 : m1;
@@ -288,10 +290,11 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int64_t t, i
     const float above = ahead ? other - mine : gap;
     gap = above < gap ? above : gap;
   }
-  bool near;
-  uint32_t kept = groups_within<float, L>(a, l, tok, mine, rank, gap, near);
+  uint32_t kept = groups_within<float, L>(a, l, tok, mine, rank);
   if constexpr (ARITH) {
-    if (__any(near)) {
+    // is the first group dropped too close to the last one kept for fp32?
+    const float margin = margin_of(a, team_reduce<L>(largest, MaxK()));
+    if (__any(l < a.n_group && mine > none<float>() && rank == a.topk_group && gap <= margin)) {
       const float low = l < a.n_group ? second[l] : none<float>();
       kept = keep_groups_exactly<L>(a, l, tok, buf, low - margin_of(a, low), exact_key<L>(a, t, l, true));
     }

@@ -106,6 +106,18 @@ def test_neighbours_closer_than_fp32(F, score):
     check(F, x, 8, b, score=score, n_group=4, topk_group=2, group_top=2)
 
 
+def test_large_biases_that_cancel_in_a_group(F):
+    """One expert of each group is pushed up by 64 and the others down: the groups' sums are
+    small while fp32 rounds each key to steps of 2^-17."""
+    rng = np.random.default_rng(13)
+    x = torch.from_numpy((rng.normal(0, 1, (400, 1)) + rng.normal(0, 2.0 ** -14, (400, 32))).astype(np.float32))
+    b = np.full(32, -64.0, np.float32)
+    b[rng.integers(0, 8, 4) + 8 * np.arange(4)] = 64.0
+    for score in ("softmax", "sigmoid"):
+        check(F, x, 4, torch.from_numpy(b), score=score, n_group=4, topk_group=2, group_top=2)
+        check(F, x, 4, torch.from_numpy(b), score=score)
+
+
 def test_masks_and_infinities(F):
     rng = np.random.default_rng(12)
     x = rng.normal(0, 1, (80, 48)).astype(np.float32)
