@@ -85,7 +85,11 @@ class Call {
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
     return v;
   }
-  bool flag() { return PyObject_IsTrue(args_[at_++]) == 1; }
+  bool flag() {
+    const int v = PyObject_IsTrue(args_[at_++]);
+    if (v < 0) throw python_error();
+    return v != 0;
+  }
   bool none(Py_ssize_t ahead = 0) const { return args_[at_ + ahead] == Py_None; }
 
   // Type, rank, place and layout of an input; the first one decides the device.

@@ -183,3 +183,10 @@ def test_buffers_and_refusals_of_the_binding(ex):
             (lambda: F.f8f8bf16_rmsnorm_quantize(None, w), "tensor")]:
         with pytest.raises(ValueError, match=text):
             call()
+    class Undecided:
+        def __bool__(self):
+            raise KeyError("undecided")
+    with pytest.raises(KeyError, match="undecided"):
+        F.f8f8bf16_rmsnorm_quantize(x, w, want_y=Undecided())
+    with pytest.raises(TypeError):
+        F.f8f8bf16_rmsnorm_quantize(x, w, eps="small")

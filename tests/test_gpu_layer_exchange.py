@@ -161,3 +161,14 @@ def test_offsets_past_31_bits(F):
     dy1, dw1 = F.f8f8bf16_moe_combine_backward(dout, near, w, rows)
     dy2, dw2 = F.f8f8bf16_moe_combine_backward(dout, dst, w, y, dY=y)
     assert torch.equal(dw1, dw2) and torch.equal(dy2[dst.long().view(-1)], dy1)
+
+
+def test_dispatch_past_31_bits(F):
+    R, K, T, k = 300_000, 8192, 30, 3
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randint(0, 256, (T, K), dtype=torch.uint8, device="cuda", generator=g)
+    s = torch.rand((T, K // 128), device="cuda", generator=g)
+    dst = (R - 1 - torch.randperm(500, generator=g, device="cuda")[:T * k]).to(torch.int32).view(T, k)
+    out, scales = F.f8f8bf16_moe_dispatch(q, s, dst, rows=R)
+    assert torch.equal(out[dst.long()], q[:, None].expand(T, k, K))
+    assert torch.equal(scales[dst.long()], s[:, None].expand(T, k, K // 128))

@@ -203,3 +203,29 @@ def test_backward_with_masked_logits(F):
             d = F.f8f8bf16_route_backward(x.cuda(), ids.cuda(), torch.ones(3, 3, device="cuda"), score=score, renormalize=renorm)
             want, size = L.route_backward(x.double().numpy(), ids.numpy(), np.ones((3, 3)), score, renorm)
             P.assert_close(d, want, REL * size + 1e-37)
+
+
+def test_offsets_past_31_bits(F):
+    """Logits past element 2^31, more tokens per workgroup than one pass, and a plan of 18
+    million pairs."""
+    T, E, k = 9_000_000, 256, 2
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.empty((T, E), dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=g)
+    r = F.f8f8bf16_route(x, k)
+    tail = F.f8f8bf16_route(x[-100:].contiguous(), k)
+    assert torch.equal(r.ids[-100:], tail.ids) and torch.equal(r.weights[-100:], tail.weights)
+    flat = r.ids.view(-1)
+    assert torch.equal(r.M_sizes, torch.bincount(flat, minlength=E))
+    starts = torch.cumsum(r.M_sizes, 0) - r.M_sizes
+    dst = r.dst_row.view(-1).long()
+    place = torch.zeros(T * k, dtype=torch.bool, device="cuda")
+    place[dst] = True
+    assert bool(place.all())                                  # a permutation
+    order = torch.sort(flat.to(torch.int16), stable=True).indices
+    assert torch.equal(dst[order], torch.arange(T * k, device="cuda"))
+    assert bool((dst >= starts[flat.long()]).all())
+    dw = torch.rand((T, k), device="cuda", generator=g)
+    d = F.f8f8bf16_route_backward(x, r.ids, dw)
+    e = F.f8f8bf16_route_backward(x[-100:].contiguous(), tail.ids, dw[-100:].contiguous())
+    assert torch.equal(d[-100:], e)

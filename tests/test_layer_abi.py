@@ -161,3 +161,23 @@ def test_layer_error_is_per_thread_and_cleared():
     t.join()
     assert seen == [""]
     assert norm(rows=0) == OK and F.layer_last_error() == ""
+
+
+def test_missing_binding_raises(monkeypatch):
+    """There is no fallback: without the compiled module the calls raise."""
+    from fp8_rowwise_scaled_amd import layer
+
+    def gone(name, package=None):
+        raise ImportError("no such file")
+    monkeypatch.setattr(layer, "_module", None)
+    monkeypatch.setattr(layer.importlib, "import_module", gone)
+    with pytest.raises(RuntimeError, match="no fallback"):
+        F.f8f8bf16_moe_combine(torch.zeros((4, 16), dtype=torch.bfloat16), torch.zeros((2, 2), dtype=torch.int32))
+
+
+def test_arguments_of_the_wrong_kind():
+    with pytest.raises(ValueError, match="must be a tensor"):
+        F.f8f8bf16_moe_combine([1, 2], None)
+    with pytest.raises(ValueError, match="must be a tensor"):
+        F.f8f8bf16_route(None, 2)
+
