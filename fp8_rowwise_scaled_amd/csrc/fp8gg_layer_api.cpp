@@ -192,7 +192,7 @@ int64_t f8f8bf16_route_workspace(int64_t T, int64_t E, int64_t k) {
   (void)k;
   if (T <= 0 || E <= 0 || T > kMaxDim || E > 1024) return 0;
   const int64_t tokens = fp8gg::route_block_tokens(T), blocks = (T + tokens - 1) / tokens;
-  return blocks > 1 ? blocks * E * 4 : 0;
+  return blocks > 1 ? blocks * fp8gg::count_row(E) * 4 : 0;
 }
 
 // Sizes and enumerations shared by route and its gradient.

@@ -46,12 +46,12 @@ struct RouteArgs {
   int32_t* ids;
   int64_t* M_sizes;             // null: no plan
   int32_t* dst_row;
-  int32_t* hist;                // [blocks, E], unless one block covers every token
+  int32_t* hist;                // [blocks, count_row(E)], unless one block covers every token
   int64_t T;
   int32_t E, k;
   int32_t n_group, topk_group, group_top;
   int32_t bf16, sigmoid, renormalize;
-  int32_t block_tokens;         // tokens of one workgroup (a multiple of 64)
+  int32_t block_tokens;         // tokens of one workgroup
   float scale;
   int32_t token_lds;            // bytes of LDS per token (set by the launcher)
 };
@@ -135,6 +135,9 @@ struct KOffsetsArgs {
 // of dweight), and tokens of one routing workgroup.
 int norm_backward_parts(int64_t rows, int64_t K);
 int route_block_tokens(int64_t T);
+// Counts of one workgroup, rounded up to whole 128-byte lines: workgroups on different
+// XCDs write neighbouring rows.
+constexpr int count_row(int64_t E) { return (int)((E + 31) / 32 * 32); }
 
 // Rows of X that one workgroup of quantize_k_offsets takes; a chunk never holds
 // rows of two groups.

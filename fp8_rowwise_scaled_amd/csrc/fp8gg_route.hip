@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
   if (!plan) return;
   __syncthreads();
   if (!alone) {
-    if ((int)threadIdx.x < a.E) a.hist[(int64_t)blockIdx.x * a.E + threadIdx.x] = count[threadIdx.x];
+    if ((int)threadIdx.x < a.E) a.hist[(int64_t)blockIdx.x * count_row(a.E) + threadIdx.x] = count[threadIdx.x];
     return;
   }
   const int c = count[threadIdx.x];                // 0 beyond E
@@ -728,10 +728,10 @@ __global__ void __launch_bounds__(kThreads) place_kernel(RouteArgs a, int blocks
   const int width = place_width(a.E), sets = kThreads / width;
   count_pairs(w, ids, held, own);
   if (a.E % 4 == 0)
-    add_counts(reinterpret_cast<const u32x4*>(a.hist), a.E / 4, a.E / 4, width, blocks, first_block,
+    add_counts(reinterpret_cast<const u32x4*>(a.hist), count_row(a.E) / 4, a.E / 4, width, blocks, first_block,
                reinterpret_cast<u32x4*>(sums));
   else
-    add_counts(reinterpret_cast<const uint32_t*>(a.hist), a.E, a.E, width, blocks, first_block,
+    add_counts(reinterpret_cast<const uint32_t*>(a.hist), count_row(a.E), a.E, width, blocks, first_block,
                reinterpret_cast<uint32_t*>(sums));
   __syncthreads();
   int total = 0, earlier = 0;
@@ -857,8 +857,9 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
 }  // namespace
 
 int route_block_tokens(int64_t T) {
-  const int64_t n = (T + 64 * kMaxBlocks - 1) / (64 * kMaxBlocks);
-  return (int)(64 * (n > 0 ? n : 1));
+  if (T <= 64) return 64;                                // one workgroup, one launch
+  if (T <= 16 * kMaxBlocks) return 16;
+  return (int)(64 * ((T + 64 * kMaxBlocks - 1) / (64 * kMaxBlocks)));
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
