@@ -46,7 +46,7 @@ struct RouteArgs {
   int32_t* ids;
   int64_t* M_sizes;             // null: no plan
   int32_t* dst_row;
-  int32_t* hist;                // [blocks, count_row(E)], unless one block covers every token
+  int32_t* hist;                // [blocks, count_row(E)]; null up to kLonePairs pairs
   int64_t T;
   int32_t E, k;
   int32_t n_group, topk_group, group_top;
@@ -135,6 +135,8 @@ struct KOffsetsArgs {
 // of dweight), and tokens of one routing workgroup.
 int norm_backward_parts(int64_t rows, int64_t K);
 int route_block_tokens(int64_t T);
+// Up to so many (token, expert) pairs one workgroup makes the plan by itself.
+constexpr int64_t kLonePairs = 4096;
 // Counts of one workgroup, rounded up to whole 128-byte lines: workgroups on different
 // XCDs write neighbouring rows.
 constexpr int count_row(int64_t E) { return (int)((E + 31) / 32 * 32); }

@@ -563,8 +563,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
   __shared__ int wave_sums[kWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int tok = lane / L;
-  const bool plan = a.M_sizes != nullptr;
   const bool alone = gridDim.x == 1 && a.block_tokens == 64;
+  const bool plan = a.M_sizes && (alone || a.hist);   // else the second kernel counts
   if (plan) {
     count[threadIdx.x] = 0;
     chosen[threadIdx.x] = -1;
@@ -671,6 +671,12 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
 // of the first one; it adds up the counts of all blocks and of those before its own,
 // then places its pairs.  At most 64 workgroups, because each of them reads all counts
 // (256 x 256 of them at 16384 tokens and 256 experts: one workgroup per block took 21 us).
+// Up to kLonePairs pairs, what its registers hold, a single workgroup counts them all
+// itself: many workgroups that read the same few lines of counts wait 3 to 5 us for them
+// (route with plan, one workgroup against many: 6.4 and 10.7 us at 256 tokens, 8 experts,
+// k = 2; 13.7 and 14.8 us at 256 tokens, 256 experts in groups, k = 8).  Fewer workgroups
+// of more pairs beyond that are slower (1024 tokens, 256 experts: 16.9 us, and 19.3 with
+// 4096 pairs each; 4096 tokens, 8 experts: 12.6 and 14.0).
 constexpr int kPlaceGroups = 64;
 
 // LDS of the second kernel: the waves' counts, and for each of the kThreads / width sets
@@ -727,18 +733,22 @@ __global__ void __launch_bounds__(kThreads) place_kernel(RouteArgs a, int blocks
   __syncthreads();
   const int width = place_width(a.E), sets = kThreads / width;
   count_pairs(w, ids, held, own);
-  if (a.E % 4 == 0)
+  if (a.hist && a.E % 4 == 0)
     add_counts(reinterpret_cast<const u32x4*>(a.hist), count_row(a.E) / 4, a.E / 4, width, blocks, first_block,
                reinterpret_cast<u32x4*>(sums));
-  else
+  else if (a.hist)
     add_counts(reinterpret_cast<const uint32_t*>(a.hist), count_row(a.E), a.E, width, blocks, first_block,
                reinterpret_cast<uint32_t*>(sums));
   __syncthreads();
   int total = 0, earlier = 0;
   if ((int)threadIdx.x < a.E) {
-    for (int s = 0; s < sets; ++s) {
-      total += sums[s * a.E + threadIdx.x];
-      earlier += sums[(sets + s) * a.E + threadIdx.x];
+    if (a.hist) {
+      for (int s = 0; s < sets; ++s) {
+        total += sums[s * a.E + threadIdx.x];
+        earlier += sums[(sets + s) * a.E + threadIdx.x];
+      }
+    } else {
+      for (int x = 0; x < kWaves; ++x) total += counts[x * a.E + threadIdx.x];
     }
     if (blockIdx.x == 0) a.M_sizes[threadIdx.x] = total;
   }
@@ -856,8 +866,12 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
 
 }  // namespace
 
+// Up to 64 tokens one workgroup chooses and plans in one launch.  Up to 4096 tokens 16 per
+// workgroup: a SIMD has one wave with four tokens rather than four of them, on four times
+// as many CUs (1024 tokens, 256 experts in groups: 15.7 us with the plan, 18.6 with 64
+// per workgroup).  Beyond that 64 or a multiple, for at most kMaxBlocks rows of counts.
 int route_block_tokens(int64_t T) {
-  if (T <= 64) return 64;                                // one workgroup, one launch
+  if (T <= 64) return 64;
   if (T <= 16 * kMaxBlocks) return 16;
   return (int)(64 * ((T + 64 * kMaxBlocks - 1) / (64 * kMaxBlocks)));
 }
@@ -869,7 +883,7 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
   const bool arith = a.bias || (a.n_group > 1 && a.group_top == 2);
   hipError_t e = arith ? launch_by_width<true>(a, blocks, stream) : launch_by_width<false>(a, blocks, stream);
   if (e != hipSuccess || !a.M_sizes || blocks == 1) return e;
-  const int span = (blocks + kPlaceGroups - 1) / kPlaceGroups;
+  const int span = a.hist ? (blocks + kPlaceGroups - 1) / kPlaceGroups : blocks;
   hipLaunchKernelGGL(place_kernel, dim3((blocks + span - 1) / span), dim3(kThreads), place_lds(a.E), stream, a,
                      blocks, span);
   return hipGetLastError();

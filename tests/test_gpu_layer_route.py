@@ -163,6 +163,25 @@ def test_many_tokens(F, T, E, k):
     assert torch.allclose(r.weights.sum(1), torch.ones(T, device="cuda"), rtol=1e-5)
 
 
+@pytest.mark.parametrize("T,E,k", [(511, 61, 8), (512, 61, 8), (513, 61, 8), (4096, 8, 1), (4097, 8, 1), (256, 1024, 16), (257, 1024, 16)])
+def test_plan_by_one_workgroup_and_by_several(F, T, E, k):
+    """Both sides of 4096 pairs, with rows that have fewer experts left than k, or none."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, E, generator=g, device="cuda")
+    x[3::7] = -torch.inf
+    x[3::14, : max(k // 2, 1)] = 1.0
+    r = F.f8f8bf16_route(x, k)
+    flat = r.ids.reshape(-1).long()
+    left = (x > -torch.inf).sum(1).clamp(max=k)
+    assert torch.equal((r.ids >= 0).sum(1), left)
+    assert torch.equal(r.M_sizes, (flat[:, None] == torch.arange(E, device="cuda")).sum(0))
+    order = torch.sort(torch.where(flat < 0, E, flat), stable=True).indices
+    n = int(left.sum())
+    want = torch.full((T * k,), -1, dtype=torch.int64, device="cuda")
+    want[order[:n]] = torch.arange(n, device="cuda")
+    assert torch.equal(r.dst_row.view(-1).long(), want)
+
+
 def test_no_tokens_and_no_plan(F):
     r = F.f8f8bf16_route(torch.empty((0, 8), device="cuda"), 2)
     assert torch.equal(r.M_sizes, torch.zeros(8, dtype=torch.int64, device="cuda")) and r.ids.shape == (0, 2)

@@ -77,10 +77,10 @@ def test_route_refusals(kw, status, text):
     assert route(**kw) == status and text in F.layer_last_error()
 
 
-def test_route_workspace_is_needed_from_the_second_block_on():
+def test_route_workspace():
+    """Counts of at most 256 workgroups, however many tokens; none for a few pairs."""
     ws = lib().f8f8bf16_route_workspace
-    assert ws(64, 256, 8) == 0 and ws(65, 256, 8) >= 2 * 256 * 4 and ws(65, 9, 2) >= 2 * 9 * 4
-    # at most 256 blocks of counts, however many tokens
+    assert ws(64, 256, 8) == 0 and ws(512, 256, 8) == 0 and ws(513, 256, 8) >= 2 * 256 * 4 and ws(5000, 9, 1) >= 2 * 9 * 4
     assert ws(16384, 256, 8) == ws(1 << 20, 256, 8) == 256 * 256 * 4
 
 
