@@ -190,8 +190,7 @@ fp8gg_status f8f8bf16_rmsnorm_backward(const uint16_t* dY, const uint16_t* H, co
 
 int64_t f8f8bf16_route_workspace(int64_t T, int64_t E, int64_t k) {
   if (T <= 0 || E <= 0 || k <= 0 || T > kMaxDim || E > 1024 || k > 16 || T * k <= fp8gg::kLonePairs) return 0;
-  const int64_t tokens = fp8gg::route_block_tokens(T), blocks = (T + tokens - 1) / tokens;
-  return blocks * fp8gg::count_row(E) * 4;
+  return fp8gg::route_count_rows(T) * fp8gg::count_row(E) * 4;
 }
 
 // Sizes and enumerations shared by route and its gradient.
@@ -234,10 +233,10 @@ fp8gg_status f8f8bf16_route(const void* logits, int logits_dtype, const float* b
                    {"M_sizes", M_sizes, 8 * E, 8, true, true},
                    {"dst_row", dst_row, 4 * T * k, 4, true, true},
                    {"workspace", workspace, need, 16, true, true}}));
-  const fp8gg::RouteArgs a{logits, bias, weights, ids, M_sizes, dst_row, need > 0 ? static_cast<int32_t*>(workspace) : nullptr, T,
-                           (int32_t)E, (int32_t)k, (int32_t)n_group, (int32_t)topk_group, group_top,
+  const fp8gg::RouteArgs a{logits, bias, weights, ids, M_sizes, dst_row,
+                           need > 0 ? static_cast<int32_t*>(workspace) : nullptr, T, (int32_t)E, (int32_t)k, (int32_t)n_group, (int32_t)topk_group, group_top,
                            logits_dtype == FP8GG_DTYPE_BF16, score == FP8GG_SCORE_SIGMOID, renormalize != 0,
-                           fp8gg::route_block_tokens(T), scale, 0};
+                           scale, 0, 0, 0, false};
   return launched(fp8gg::launch_route(a, static_cast<hipStream_t>(stream)), "route");
 }
 

@@ -51,9 +51,12 @@ struct RouteArgs {
   int32_t E, k;
   int32_t n_group, topk_group, group_top;
   int32_t bf16, sigmoid, renormalize;
-  int32_t block_tokens;         // tokens of one workgroup
   float scale;
-  int32_t token_lds;            // bytes of LDS per token (set by the launcher)
+  // set by the launcher
+  int32_t block_tokens;         // tokens of one workgroup
+  int32_t threads;              // blockDim.x, here because the other arguments are loaded anyway
+  int32_t token_lds;            // bytes of LDS per token
+  bool alone;                   // one workgroup chooses and plans
 };
 
 struct RouteBackwardArgs {
@@ -134,7 +137,7 @@ struct KOffsetsArgs {
 // Teams that the norm's backward pass spreads its rows over (rows of its partial sums
 // of dweight), and tokens of one routing workgroup.
 int norm_backward_parts(int64_t rows, int64_t K);
-int route_block_tokens(int64_t T);
+int64_t route_count_rows(int64_t T);
 // Up to so many (token, expert) pairs one workgroup makes the plan by itself.
 constexpr int64_t kLonePairs = 4096;
 // Counts of one workgroup, rounded up to whole 128-byte lines: workgroups on different

@@ -229,8 +229,8 @@ __device__ __forceinline__ uint32_t keep_groups_exactly(const RouteArgs& a, int 
 
 // The groups kept, by way of the token's own LDS: kMaxGroups best and second keys and E +
 // n_group keys (one word of padding per group keeps the lanes that scan the groups on
-// different banks).  Only this wave touches it.  Two lanes scan a group where there are
-// enough.  ARITH: the keys are fp32 sums, and a border too close is decided in fp64.
+// different banks).  Only this wave touches it.  Up to eight lanes scan a group where there
+// are enough.  ARITH: the keys are fp32 sums, and a border too close is decided in fp64.
 template <int L, int V, bool ARITH>
 __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int64_t t, int l, int tok, float* lds,
                                                 const float (&key)[V]) {
@@ -246,8 +246,8 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int64_t t, i
       if (expert_of<L>(v, l) < a.E) buf[expert_of<L>(v, l) + group(expert_of<L>(v, l))] = key[v];
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  const bool pairs = 2 * a.n_group <= L;
-  const int g = pairs ? l >> 1 : l, step = pairs ? 2 : 1;
+  const int shift = 8 * a.n_group <= L ? 3 : 4 * a.n_group <= L ? 2 : 2 * a.n_group <= L ? 1 : 0;
+  const int g = l >> shift, step = 1 << shift;
   float m1 = none<float>(), m2 = none<float>();
   const auto take = [&](float x) {
     const float low = x < m1 ? x : m1;
@@ -256,13 +256,15 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int64_t t, i
   };
   if (g < a.n_group) {
 #pragma unroll 8
-    for (int i = pairs ? l & 1 : 0; i < per; i += step) take(buf[g * (per + 1) + i]);
+    for (int i = l & (step - 1); i < per; i += step) take(buf[g * (per + 1) + i]);
   }
-  if (pairs) {
-    const float o1 = dpp<0xB1>(m1), o2 = dpp<0xB1>(m2);
+  const auto join = [&](float o1, float o2) {
     take(o1);
     m2 = o2 > m2 ? o2 : m2;
-  }
+  };
+  if (shift > 0) join(dpp<0xB1>(m1), dpp<0xB1>(m2));       // lanes 1 0 3 2
+  if (shift > 1) join(dpp<0x4E>(m1), dpp<0x4E>(m2));       // lanes 2 3 0 1
+  if (shift > 2) join(dpp<0x141>(m1), dpp<0x141>(m2));     // mirror in each half row
   // A sum may be far smaller than what was added: its error goes by the largest key.
   float largest = 0.f;
   if (ARITH && g < a.n_group) {
@@ -349,8 +351,8 @@ struct alignas(16) Candidates {
   int chosen[kMaxChosen];
 };
 
-// Lower bound of the k-th largest key: the k-th largest of 16 lanes' maxima (of the four
-// rows' bounds the best one).  -infinity where fewer than k lanes hold a key.
+// Lower bound of the k-th largest key: the k-th largest of the team's lanes' maxima.
+// -infinity where fewer than k lanes hold a key.
 template <int N>
 __device__ __forceinline__ int count_reaching(float m, float other_than) {
   // lanes N, N - 1, ... 1 further along the row
@@ -363,7 +365,21 @@ __device__ __forceinline__ float bound_of(int k, const float (&key)[V]) {
   float m = key[0];
 #pragma unroll
   for (int v = 1; v < V; ++v) m = MaxK()(m, key[v]);
-  const int reaching = 1 + count_reaching<15>(m, m);
+  int reaching;
+  if constexpr (L == 16) {
+    reaching = 1 + count_reaching<15>(m, m);
+  } else {
+    uint32_t rows[4], a, b;                        // the maxima of the wave's four rows
+    swapped<false>(__float_as_uint(m), a, b);
+    swapped<true>(a, rows[0], rows[1]);
+    swapped<true>(b, rows[2], rows[3]);
+    reaching = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = __uint_as_float(rows[i]);
+      reaching += (x >= m) + count_reaching<15>(x, m);
+    }
+  }
   return team_reduce<L>(reaching >= k ? m : none<float>(), MaxK());
 }
 
@@ -556,22 +572,22 @@ __device__ __forceinline__ float shifted_sigmoid(float x, float most, bool mine)
 
 template <int L, int V, bool ARITH>
 __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
-  constexpr int kTokens = kWaves * (64 / L);       // tokens of one pass over the workgroup's waves
+  const int pass = a.threads / L;                  // tokens of one pass over the workgroup's waves
   extern __shared__ double dynamic_lds[];
   __shared__ int count[kMaxExperts];
   __shared__ int chosen[64 * kMaxChosen];
   __shared__ int wave_sums[kWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int tok = lane / L;
-  const bool alone = gridDim.x == 1 && a.block_tokens == 64;
+  const bool alone = a.alone;
   const bool plan = a.M_sizes && (alone || a.hist);   // else the second kernel counts
   if (plan) {
-    count[threadIdx.x] = 0;
-    chosen[threadIdx.x] = -1;
+    for (int e = threadIdx.x; e < a.E; e += a.threads) count[e] = 0;
+    if (alone) chosen[threadIdx.x] = -1;
     __syncthreads();
   }
   const int64_t first = (int64_t)blockIdx.x * a.block_tokens;
-  for (int at = wave * (64 / L); at < a.block_tokens; at += kTokens) {
+  for (int at = wave * (64 / L); at < a.block_tokens; at += pass) {
     if (first + at >= a.T) break;                  // uniform over the wave
     // Opaque to the compiler in each pass: it would keep what follows from the lane for
     // every v (expert, group, addresses) in registers across the passes, of which there
@@ -631,9 +647,19 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) most = MaxK()(most, x[v]);
       most = team_reduce<L>(most, MaxK());
+      // In the order of a team of 64 lanes, whichever the team: the weights do not depend
+      // on how many tokens a call has.
+      constexpr int kRows = L == 16 && V >= 4 ? 4 : 1;
+      float part[kRows] = {};
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum += x[v] > none<float>() ? expf(x[v] - most) : 0.f;
-      sum = team_reduce<L>(sum, AddF());
+      for (int v = 0; v < V; ++v) part[v % kRows] += x[v] > none<float>() ? expf(x[v] - most) : 0.f;
+      if constexpr (kRows == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[i] = row16_reduce(part[i], AddF());
+        sum = (part[0] + part[1]) + (part[2] + part[3]);
+      } else {
+        sum = team_reduce<L>(part[0], AddF());
+      }
       p = mine ? expf(lx - most) / sum : 0.f;
     }
     if (live && l < a.k) {
@@ -648,10 +674,10 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
   if (!plan) return;
   __syncthreads();
   if (!alone) {
-    if ((int)threadIdx.x < a.E) a.hist[(int64_t)blockIdx.x * count_row(a.E) + threadIdx.x] = count[threadIdx.x];
+    for (int e = threadIdx.x; e < a.E; e += a.threads) a.hist[(int64_t)blockIdx.x * count_row(a.E) + e] = count[e];
     return;
   }
-  const int c = count[threadIdx.x];                // 0 beyond E
+  const int c = (int)threadIdx.x < a.E ? count[threadIdx.x] : 0;
   const int before = prefix_before(c, wave_sums);
   if ((int)threadIdx.x < a.E) a.M_sizes[threadIdx.x] = c;
   int* counts = reinterpret_cast<int*>(dynamic_lds);
@@ -763,23 +789,27 @@ hipError_t launch(const RouteArgs& a, int blocks, hipStream_t stream) {
   const int keys = a.n_group > 1 ? (2 * kMaxGroups + a.E + a.n_group) * (int)sizeof(float) : 0;
   RouteArgs b = a;
   b.token_lds = ((keys > (int)sizeof(Candidates) ? keys : (int)sizeof(Candidates)) + 15) / 16 * 16;
-  const size_t tokens = (size_t)kWaves * (64 / L) * b.token_lds;
-  const size_t counts = a.M_sizes && blocks == 1 ? (size_t)kWaves * a.E * sizeof(int) : 0;
-  hipLaunchKernelGGL((route_kernel<L, V, ARITH>), dim3(blocks), dim3(kThreads), tokens > counts ? tokens : counts, stream,
+  const size_t tokens = (size_t)(a.threads / L) * b.token_lds;
+  const size_t counts = a.alone ? (size_t)kWaves * a.E * sizeof(int) : 0;
+  hipLaunchKernelGGL((route_kernel<L, V, ARITH>), dim3(blocks), dim3(a.threads), tokens > counts ? tokens : counts, stream,
                      b);
   return hipGetLastError();
 }
 
 template <bool ARITH>
-hipError_t launch_by_width(const RouteArgs& a, int blocks, hipStream_t stream) {
+hipError_t launch_by_width(const RouteArgs& a, bool wide, int blocks, hipStream_t stream) {
+  if (wide) {
+    if (a.E <= 128) return launch<64, 2, ARITH>(a, blocks, stream);
+    if (a.E <= 256) return launch<64, 4, ARITH>(a, blocks, stream);
+    if (a.E <= 512) return launch<64, 8, ARITH>(a, blocks, stream);
+    return launch<64, 16, ARITH>(a, blocks, stream);
+  }
   if (a.E <= 16) return launch<16, 1, ARITH>(a, blocks, stream);
   if (a.E <= 32) return launch<16, 2, ARITH>(a, blocks, stream);
   if (a.E <= 64) return launch<16, 4, ARITH>(a, blocks, stream);
   if (a.E <= 128) return launch<16, 8, ARITH>(a, blocks, stream);
   if (a.E <= 256) return launch<16, 16, ARITH>(a, blocks, stream);
-  // 16384 tokens, k = 8, us: 384 experts on 16 lanes 27.0, on 64 lanes 39.9; 512: 25.2, 37.4
-  if (a.E <= 512) return launch<16, 32, ARITH>(a, blocks, stream);
-  return launch<64, 16, ARITH>(a, blocks, stream);
+  return launch<16, 32, ARITH>(a, blocks, stream);
 }
 
 // One wave per token.  Only the chosen logits matter, except for softmax weights that
@@ -866,23 +896,52 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
 
 }  // namespace
 
-// Up to 64 tokens one workgroup chooses and plans in one launch.  Up to 4096 tokens 16 per
-// workgroup: a SIMD has one wave with four tokens rather than four of them, on four times
-// as many CUs (1024 tokens, 256 experts in groups: 15.7 us with the plan, 18.6 with 64
-// per workgroup).  Beyond that 64 or a multiple, for at most kMaxBlocks rows of counts.
-int route_block_tokens(int64_t T) {
-  if (T <= 64) return 64;
+// How the tokens are shared out.  16 lanes per token take the fewest instructions; 64 lanes
+// have the shorter chain of them and are the faster ones until the SIMDs are full.  Graph of
+// calls with 256 experts in 8 groups, k = 8, sigmoid and bias, us, against 16 lanes and 16
+// (up to 64 tokens: all) tokens per workgroup:
+//   1 token         one launch, 64 lanes          8.1 against 10.3
+//   8               one launch, 64 lanes          9.1 against 9.5 in two launches
+//   16 to 512       4 tokens per workgroup of 256 threads, then one workgroup that counts:
+//                   16: 9.8 against 11.0; 64: 9.9 and 15.0; 200: 10.9 and 13.8
+//   1024 (4096)     16 tokens of 64 lanes per workgroup: 15.5 (17.6) against 16.6 (21.8)
+//   16384           16 lanes: 24.6, and 40.2 with 64
+// 344 experts: 16 tokens 11.3 against 19.4.  Up to 128 experts 16 lanes stay the better ones
+// where counts are handed on (4096 tokens, 128 experts: 12.8 and 14.2 with 64), and up to 64
+// experts everywhere.  Without a plan 4 tokens per workgroup up to 2048 (8.3 against 9.4).
+//
+// Tokens of one workgroup where there are counts to hand on, at most kMaxBlocks rows.
+static int counted_tokens(int64_t T) {
   if (T <= 16 * kMaxBlocks) return 16;
   return (int)(64 * ((T + 64 * kMaxBlocks - 1) / (64 * kMaxBlocks)));
 }
 
-hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
+int64_t route_count_rows(int64_t T) { return (T + counted_tokens(T) - 1) / counted_tokens(T); }
+
+hipError_t launch_route(const RouteArgs& given, hipStream_t stream) {
+  RouteArgs a = given;
   if (a.T == 0 && !a.M_sizes) return hipSuccess;
+  a.alone = a.M_sizes && a.T <= 64 && a.T * a.E <= (a.E <= 128 ? 4096 : 2048);
+  bool wide;
+  a.threads = 256;
+  if (a.alone) {
+    a.block_tokens = 64;
+    wide = a.E > 128;
+    a.threads = kThreads;
+  } else if (!a.hist && a.E > 64 && a.T <= 8 * kMaxBlocks) {
+    a.block_tokens = 4;
+    wide = true;
+  } else {
+    a.block_tokens = counted_tokens(a.T);
+    wide = a.E > (a.block_tokens == 16 ? 128 : 512);
+    if (wide || a.block_tokens > 16) a.threads = kThreads;
+  }
   // T == 0 with a plan: one workgroup writes zero counts
   const int blocks = a.T == 0 ? 1 : (int)((a.T + a.block_tokens - 1) / a.block_tokens);
   const bool arith = a.bias || (a.n_group > 1 && a.group_top == 2);
-  hipError_t e = arith ? launch_by_width<true>(a, blocks, stream) : launch_by_width<false>(a, blocks, stream);
-  if (e != hipSuccess || !a.M_sizes || blocks == 1) return e;
+  hipError_t e = arith ? launch_by_width<true>(a, wide, blocks, stream)
+                       : launch_by_width<false>(a, wide, blocks, stream);
+  if (e != hipSuccess || !a.M_sizes || a.alone) return e;
   const int span = a.hist ? (blocks + kPlaceGroups - 1) / kPlaceGroups : blocks;
   hipLaunchKernelGGL(place_kernel, dim3((blocks + span - 1) / span), dim3(kThreads), place_lds(a.E), stream, a,
                      blocks, span);

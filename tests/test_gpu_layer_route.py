@@ -182,6 +182,22 @@ def test_plan_by_one_workgroup_and_by_several(F, T, E, k):
     assert torch.equal(r.dst_row.view(-1).long(), want)
 
 
+@pytest.mark.parametrize("E", [8, 60, 100, 128, 200, 256, 300, 512, 700])
+@pytest.mark.parametrize("score,renormalize", [("softmax", False), ("softmax", True), ("sigmoid", False)])
+def test_rows_do_not_depend_on_the_batch(F, E, score, renormalize):
+    """The same bits, however many tokens a call has and with or without the plan."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    x = torch.randn(20000, E, generator=g, device="cuda")
+    b = 0.1 * torch.randn(E, generator=g, device="cuda")
+    kw = dict(bias=b, score=score, renormalize=renormalize, n_group=4, topk_group=3, group_top=2)
+    all_of = F.f8f8bf16_route(x, 5, **kw)
+    for start, n in [(0, 1), (3, 6), (9, 17), (64, 64), (100, 200), (300, 1000), (2000, 4096), (10000, 5000)]:
+        for plan in (True, False):
+            r = F.f8f8bf16_route(x[start : start + n], 5, plan=plan, **kw)
+            assert torch.equal(r.ids, all_of.ids[start : start + n]), (start, n, plan)
+            assert torch.equal(r.weights, all_of.weights[start : start + n]), (start, n, plan)
+
+
 def test_no_tokens_and_no_plan(F):
     r = F.f8f8bf16_route(torch.empty((0, 8), device="cuda"), 2)
     assert torch.equal(r.M_sizes, torch.zeros(8, dtype=torch.int64, device="cuda")) and r.ids.shape == (0, 2)
