@@ -190,7 +190,7 @@ fp8gg_status f8f8bf16_rmsnorm_backward(const uint16_t* dY, const uint16_t* H, co
 
 int64_t f8f8bf16_route_workspace(int64_t T, int64_t E, int64_t k) {
   if (T <= 0 || E <= 0 || k <= 0 || T > kMaxDim || E > 1024 || k > 16 || T * k <= fp8gg::kLonePairs) return 0;
-  return fp8gg::route_count_rows(T) * fp8gg::count_row(E) * 4;
+  return fp8gg::route_count_rows(T, E) * fp8gg::count_row(E) * 4;
 }
 
 // Sizes and enumerations shared by route and its gradient.

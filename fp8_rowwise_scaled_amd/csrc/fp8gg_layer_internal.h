@@ -137,7 +137,7 @@ struct KOffsetsArgs {
 // Teams that the norm's backward pass spreads its rows over (rows of its partial sums
 // of dweight), and tokens of one routing workgroup.
 int norm_backward_parts(int64_t rows, int64_t K);
-int64_t route_count_rows(int64_t T);
+int64_t route_count_rows(int64_t T, int64_t E);
 // Up to so many (token, expert) pairs one workgroup makes the plan by itself.
 constexpr int64_t kLonePairs = 4096;
 // Counts of one workgroup, rounded up to whole 128-byte lines: workgroups on different

@@ -910,20 +910,26 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
 // where counts are handed on (4096 tokens, 128 experts: 12.8 and 14.2 with 64), and up to 64
 // experts everywhere.  Without a plan 4 tokens per workgroup up to 2048 (8.3 against 9.4).
 //
-// Tokens of one workgroup where there are counts to hand on, at most kMaxBlocks rows.
-static int counted_tokens(int64_t T) {
-  if (T <= 16 * kMaxBlocks) return 16;
+// Tokens of one workgroup where there are counts to hand on, at most kMaxBlocks rows: each
+// place workgroup reads all of them, so where the choice is quick half as many rows are
+// better (4096 tokens, k = 2, 8 experts: 10.8 us with 32 tokens, 12.7 with 16; 128 experts,
+// k = 8: 12.9 and 13.9; but 256 experts: 17.0 and 14.6).
+static int counted_tokens(int64_t T, int64_t E) {
+  if (T <= (E <= 128 ? 8 : 16) * kMaxBlocks) return 16;
+  if (T <= 16 * kMaxBlocks) return 32;
   return (int)(64 * ((T + 64 * kMaxBlocks - 1) / (64 * kMaxBlocks)));
 }
 
-int64_t route_count_rows(int64_t T) { return (T + counted_tokens(T) - 1) / counted_tokens(T); }
+int64_t route_count_rows(int64_t T, int64_t E) {
+  const int tokens = counted_tokens(T, E);
+  return (T + tokens - 1) / tokens;
+}
 
 hipError_t launch_route(const RouteArgs& given, hipStream_t stream) {
   RouteArgs a = given;
   if (a.T == 0 && !a.M_sizes) return hipSuccess;
   a.alone = a.M_sizes && a.T <= 64 && a.T * a.E <= (a.E <= 128 ? 4096 : 2048);
   bool wide;
-  a.threads = 256;
   if (a.alone) {
     a.block_tokens = 64;
     wide = a.E > 128;
@@ -931,10 +937,12 @@ hipError_t launch_route(const RouteArgs& given, hipStream_t stream) {
   } else if (!a.hist && a.E > 64 && a.T <= 8 * kMaxBlocks) {
     a.block_tokens = 4;
     wide = true;
+    a.threads = 256;
   } else {
-    a.block_tokens = counted_tokens(a.T);
+    a.block_tokens = counted_tokens(a.T, a.E);
     wide = a.E > (a.block_tokens == 16 ? 128 : 512);
-    if (wide || a.block_tokens > 16) a.threads = kThreads;
+    if (wide || a.block_tokens > 32) a.threads = kThreads;
+    else a.threads = 16 * a.block_tokens;
   }
   // T == 0 with a plan: one workgroup writes zero counts
   const int blocks = a.T == 0 ? 1 : (int)((a.T + a.block_tokens - 1) / a.block_tokens);
