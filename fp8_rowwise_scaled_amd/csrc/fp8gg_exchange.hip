@@ -18,6 +18,20 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kMaxGrid = 1 << 20;
 
+// Pieces of a row of nvec vectors, one workgroup each, and the threads of a workgroup: as
+// many waves as have something to do, since those without take the place of others on the
+// CU (us, and with 256 threads whatever the row: combine, 6696 tokens x 8 x 416: 11.6,
+// 18.2; 3650 x 1 x 4512: 19.4, 22.6; dispatch, 4096 x 8 x 256 codes: 5.1, 7.4; combine's
+// gradients, 6696 x 8 x 416: 17.8, 29.3).
+struct Split {
+  int chunks, threads;
+};
+Split split_row(int nvec) {
+  const int waves = nvec > 0 ? (nvec + 63) / 64 : 1;
+  const int chunks = (waves + kThreads / 64 - 1) / (kThreads / 64);
+  return {chunks, (waves + chunks - 1) / chunks * 64};
+}
+
 // Places and weights of one token, the j-th in lane j (k <= 64).  Read with every lane
 // of the wave active.
 struct Places {
@@ -38,13 +52,13 @@ __device__ __forceinline__ float weight_of(const Places& p, int j) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p.weight), j));
 }
 
-// One workgroup copies 4 KiB of one token's codes (16 bytes per thread) to its k places.
-__global__ void __launch_bounds__(kThreads) dispatch_kernel(DispatchArgs a, int chunks, int64_t work) {
+// One workgroup copies up to 4 KiB of one token's codes (16 bytes per thread) to its k places.
+__global__ void __launch_bounds__(kThreads) dispatch_kernel(DispatchArgs a, Split split, int64_t work) {
   const int nvec = a.K / 16;
   for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-    const int64_t t = i / chunks;
-    const int c = (int)(i - t * chunks);
-    const int v = c * kThreads + threadIdx.x;
+    const int64_t t = i / split.chunks;
+    const int c = (int)(i - t * split.chunks);
+    const int v = c * split.threads + threadIdx.x;
     u32x4 x = {0, 0, 0, 0};
     if (v < nvec) x = reinterpret_cast<const u32x4*>(a.XQ)[t * nvec + v];
     const Places p = load_places(a.dst_row, nullptr, t, a.k);
@@ -54,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(DispatchArgs a, int 
       if (v < nvec) store_out(reinterpret_cast<u32x4*>(a.XQs) + r * nvec + v, x);
     }
     if (c == 0) {
-      for (int s = threadIdx.x; s < a.scale_cols; s += kThreads) {
+      for (int s = threadIdx.x; s < a.scale_cols; s += split.threads) {
         const float scale = a.x_scale[t * a.scale_cols + s];
         for (int j = 0; j < a.k; ++j) {
           const int64_t r = row_of(p, j);
@@ -65,13 +79,13 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(DispatchArgs a, int 
   }
 }
 
-// One workgroup sums 2048 columns of one token, eight per thread.
+// One workgroup sums up to 2048 columns of one token, eight per thread.
 template <bool STREAM>
-__global__ void __launch_bounds__(kThreads) combine_kernel(ExchangeArgs a, int chunks, int64_t work) {
+__global__ void __launch_bounds__(kThreads) combine_kernel(ExchangeArgs a, Split split, int64_t work) {
   const int nvec = a.N / 8;
   for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-    const int64_t t = i / chunks;
-    const int v = (int)(i - t * chunks) * kThreads + threadIdx.x;
+    const int64_t t = i / split.chunks;
+    const int v = (int)(i - t * split.chunks) * split.threads + threadIdx.x;
     const bool inside = v < nvec;
     const Places p = load_places(a.dst_row, a.weights, t, a.k);
     F8 sum = {};
@@ -110,14 +124,14 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(ExchangeArgs a, int c
 
 // A workgroup takes two places of one token, both of whose rows of Y are asked for before
 // one is used or any row stored: a load that follows stores waits for them too.  NV > 0:
-// the token's row of dout stays in registers (N <= 2048 NV); NV == 0: it is read again
-// for every place.  The workgroups of one token follow each other on one XCD, whose L2
+// the token's row of dout stays in registers (N <= 2048 NV; NV == 1: as many waves as the
+// row needs, else four); NV == 0: it is read again for every place.  The workgroups of one token follow each other on one XCD, whose L2
 // holds its dout.  2047 tokens x 8 x 7168: all eight places in one workgroup 110 us, in
 // a workgroup of its own each four 98 us, each two 96 us; 90 us with STREAM.
 constexpr int kRowsAtOnce = 2;
 
 template <int NV, bool STREAM>
-__global__ void __launch_bounds__(kThreads) combine_backward_kernel(ExchangeArgs a, int batches, int64_t work) {
+__global__ void __launch_bounds__(kThreads) combine_backward_kernel(ExchangeArgs a, int waves, int batches, int64_t work) {
   __shared__ float part[2][kThreads / 64][kRowsAtOnce];
   const int nvec = a.N / 8;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -199,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(ExchangeArgs
       if (threadIdx.x < kRowsAtOnce && j0 + (int)threadIdx.x < a.k) {
         float s = 0.f;
 #pragma unroll
-        for (int x = 0; x < kThreads / 64; ++x) s += part[slot][x][threadIdx.x];
+        for (int x = 0; x < kThreads / 64; ++x) s += NV != 1 || x < waves ? part[slot][x][threadIdx.x] : 0.f;
         a.dweights[t * a.k + j0 + threadIdx.x] = s;
       }
       slot ^= 1;   // rewritten only after the next token's barrier
@@ -211,35 +225,35 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(ExchangeArgs
 
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t stream) {
   if (a.T == 0 || a.k == 0 || a.R == 0) return hipSuccess;
-  const int nvec = a.K / 16;
-  const int chunks = nvec > 0 ? (nvec + kThreads - 1) / kThreads : 1;
-  const int64_t work = a.T * chunks;
-  hipLaunchKernelGGL(dispatch_kernel, dim3((uint32_t)(work < kMaxGrid ? work : kMaxGrid)), dim3(kThreads), 0, stream, a,
-                     chunks, work);
+  const Split split = split_row(a.K / 16);
+  const int64_t work = a.T * split.chunks;
+  hipLaunchKernelGGL(dispatch_kernel, dim3((uint32_t)(work < kMaxGrid ? work : kMaxGrid)), dim3(split.threads), 0, stream,
+                     a, split, work);
   return hipGetLastError();
 }
 
 hipError_t launch_combine(const ExchangeArgs& a, hipStream_t stream) {
   if (a.T == 0 || a.N == 0) return hipSuccess;
-  const int chunks = (a.N / 8 + kThreads - 1) / kThreads;
-  const int64_t work = a.T * chunks;
-  const dim3 grid((uint32_t)(work < kMaxGrid ? work : kMaxGrid)), threads(kThreads);
+  const Split split = split_row(a.N / 8);
+  const int64_t work = a.T * split.chunks;
+  const dim3 grid((uint32_t)(work < kMaxGrid ? work : kMaxGrid)), threads(split.threads);
   if (a.T * a.k * a.N * 2 > kStreamBytes)
-    hipLaunchKernelGGL((combine_kernel<true>), grid, threads, 0, stream, a, chunks, work);
+    hipLaunchKernelGGL((combine_kernel<true>), grid, threads, 0, stream, a, split, work);
   else
-    hipLaunchKernelGGL((combine_kernel<false>), grid, threads, 0, stream, a, chunks, work);
+    hipLaunchKernelGGL((combine_kernel<false>), grid, threads, 0, stream, a, split, work);
   return hipGetLastError();
 }
 
 template <int NV>
 static hipError_t launch_back(const ExchangeArgs& a, hipStream_t stream) {
   const int batches = (a.k + kRowsAtOnce - 1) / kRowsAtOnce;
+  const int waves = NV == 1 ? split_row(a.N / 8).threads / 64 : kThreads / 64;
   const int64_t work = (a.T + 7) / 8 * 8 * batches;
-  const dim3 grid((uint32_t)(work < kMaxGrid ? work : kMaxGrid)), threads(kThreads);
+  const dim3 grid((uint32_t)(work < kMaxGrid ? work : kMaxGrid)), threads(64 * waves);
   if (a.T * a.k * a.N * 2 > kStreamBytes)
-    hipLaunchKernelGGL((combine_backward_kernel<NV, true>), grid, threads, 0, stream, a, batches, work);
+    hipLaunchKernelGGL((combine_backward_kernel<NV, true>), grid, threads, 0, stream, a, waves, batches, work);
   else
-    hipLaunchKernelGGL((combine_backward_kernel<NV, false>), grid, threads, 0, stream, a, batches, work);
+    hipLaunchKernelGGL((combine_backward_kernel<NV, false>), grid, threads, 0, stream, a, waves, batches, work);
   return hipGetLastError();
 }
 
