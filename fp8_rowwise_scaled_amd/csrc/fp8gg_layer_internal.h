@@ -134,8 +134,8 @@ struct KOffsetsArgs {
   int32_t G, K, scale_cols;
 };
 
-// Teams that the norm's backward pass spreads its rows over (rows of its partial sums
-// of dweight), and tokens of one routing workgroup.
+// Workgroups that the norm's backward pass spreads its rows over (rows of its partial sums
+// of dweight), and rows of counts that routing hands on.
 int norm_backward_parts(int64_t rows, int64_t K);
 int64_t route_count_rows(int64_t T, int64_t E);
 // Up to so many (token, expert) pairs one workgroup makes the plan by itself.

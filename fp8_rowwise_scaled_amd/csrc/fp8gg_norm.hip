@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_backward_kernel(NormB
   constexpr bool kAhead = NV == 1 || TPR == 64;
   constexpr bool kKept = NV <= 2;
   const int lane = threadIdx.x % TPR;
-  const int team = blockIdx.x * kTeams + threadIdx.x / TPR;
-  if (team >= a.parts) return;   // whole waves; teams of several waves fill their workgroup
+  const int team = blockIdx.x * kTeams + threadIdx.x / TPR, teams = a.parts * kTeams;
   const int nvec = a.K / 8;
   const float inv_k = 1.0f / (float)a.K;
   F8 held[kAhead ? NV : 1], dw[NV] = {};
@@ -211,17 +210,17 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_backward_kernel(NormB
     for (int i = 0; i < NV; ++i) {
       held[i] = F8{};
       if (i * TPR + lane < nvec) held[i] = load_weight(a.weight, a.w_f32, i * TPR + lane);
-      now[i] = load_back(a, team, i * TPR + lane);
+      if (team < a.rows) now[i] = load_back(a, team, i * TPR + lane);
     }
   }
   int slot = 0;
-  for (int64_t row = team; row < a.rows; row += a.parts) {
+  for (int64_t row = team; row < a.rows; row += teams) {
     const float rstd = a.rstd[row];
     if constexpr (kKept) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if constexpr (!kAhead) now[i] = load_back(a, row, i * TPR + lane);
-        else if (row + a.parts < a.rows) next[i] = load_back(a, row + a.parts, i * TPR + lane);
+        else if (row + teams < a.rows) next[i] = load_back(a, row + teams, i * TPR + lane);
       }
     }
     float dot = 0.f;
@@ -256,13 +255,25 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_backward_kernel(NormB
       for (int i = 0; i < NV; ++i) now[i] = next[i];
     }
   }
+  // The workgroup's sums, those of several teams joined first.
+  __shared__ f32x4 joined[kTeams > 1 ? kTeams * TPR * NV * 2 : 1];
+  f32x4* partial = reinterpret_cast<f32x4*>(a.partial + (int64_t)blockIdx.x * a.K);
+  f32x4* own = kTeams > 1 ? joined + threadIdx.x / TPR * (TPR * NV * 2) : partial;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = i * TPR + lane;
     if (j < nvec) {
-      f32x4* p = reinterpret_cast<f32x4*>(a.partial + (int64_t)team * a.K) + 2 * j;
-      p[0] = f32x4{dw[i].v[0], dw[i].v[1], dw[i].v[2], dw[i].v[3]};
-      p[1] = f32x4{dw[i].v[4], dw[i].v[5], dw[i].v[6], dw[i].v[7]};
+      own[2 * j] = f32x4{dw[i].v[0], dw[i].v[1], dw[i].v[2], dw[i].v[3]};
+      own[2 * j + 1] = f32x4{dw[i].v[4], dw[i].v[5], dw[i].v[6], dw[i].v[7]};
+    }
+  }
+  if constexpr (kTeams > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * nvec; c += threads_of(TPR)) {
+      f32x4 sum = joined[c];
+#pragma unroll
+      for (int x = 1; x < kTeams; ++x) sum += joined[x * (TPR * NV * 2) + c];
+      partial[c] = sum;
     }
   }
 }
@@ -304,9 +315,7 @@ hipError_t launch_norm(const NormArgs& a, int block, hipStream_t stream) {
 
 template <int TPR, int NV>
 hipError_t launch_back(const NormBackwardArgs& a, hipStream_t stream) {
-  constexpr int kTeams = threads_of(TPR) / TPR;
-  hipLaunchKernelGGL((rmsnorm_backward_kernel<TPR, NV>), dim3((a.parts + kTeams - 1) / kTeams),
-                     dim3(threads_of(TPR)), 0, stream, a);
+  hipLaunchKernelGGL((rmsnorm_backward_kernel<TPR, NV>), dim3(a.parts), dim3(threads_of(TPR)), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -336,10 +345,12 @@ hipError_t launch_rmsnorm_quantize(const NormArgs& given, int block, hipStream_t
 // One workgroup per compute unit of 1024 threads, two of 256 or 512; 2048 teams of one
 // wave (K = 512, 24 M elements: 37.5 us, 1024 teams 49.8, 4096 40.6, 512 of 256 threads
 // 101).  More teams read and write more partial sums (K = 2048: 512 teams 38.6, 1024
-// 40.3, 256 59.8).
+// 40.3, 256 59.8); the four one-wave teams of a workgroup join theirs
+// first (2000 x 512: 12.5 -> 8.7; 16000 x 1024: 25.6 -> 21.0).
 int norm_backward_parts(int64_t rows, int64_t K) {
-  const int64_t nvec = K / 8, teams = nvec <= 128 ? 2048 : (nvec <= 512 ? 512 : 256);
-  return (int)(rows < teams ? rows : teams);
+  const int64_t nvec = K / 8, most = nvec <= 512 ? 512 : 256, teams = nvec <= 128 ? 4 : 1;
+  const int64_t filled = (rows + teams - 1) / teams;
+  return (int)(filled < most ? filled : most);
 }
 
 hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream) {
