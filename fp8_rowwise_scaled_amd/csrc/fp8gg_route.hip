@@ -1,12 +1,12 @@
 // Routing of tokens to experts, its plan (rows per expert, places of the pairs) and
 // its gradient (gfx950).
 //
-// Choice.  A team of 16 lanes (E <= 512; else the wave's 64) holds one token's keys in
-// registers, up to 32 per lane.  The k-th largest of 16 lanes' own maxima bounds the
-// k-th largest key from below; the keys that reach it, a dozen or so of 256, go to LDS,
+// Choice.  A team of 16 or 64 lanes holds one token's keys in registers, up to 32 per
+// lane.  The k-th largest of the lanes' own maxima bounds the k-th largest key from
+// below; the keys that reach it, a dozen or so of 256, go to LDS,
 // and each of them finds its rank by comparing itself with the others.  That is about a
 // third of the instructions of k rounds of a maximum over the team (48 us at 16384
-// tokens, 256 experts in 8 groups, k = 8).
+// tokens, 256 experts in 8 groups, k = 8, against 18).
 //
 // What has to be compared exactly.  Scores rise with their logits, so without a bias
 // and with groups ranked by their best expert the logits themselves are the keys: exact
@@ -18,13 +18,16 @@
 // Plan.  A stable counting sort of the pairs by expert: each workgroup counts its
 // tokens' experts, the second kernel adds up the counts before its own block and ranks
 // the block's pairs by comparing expert numbers within a wave (ballots over their bits)
-// and counting across waves.  Integer sums only, so the order is fixed.
+// and counting across waves.  Integer sums only, so the order is fixed.  A few tokens are
+// planned by the workgroup that chooses, up to 4096 pairs by a second one that counts
+// them itself.
 //
 // 16384 tokens, 256 experts in 8 groups, k = 8, sigmoid and bias: 18 us for the choice (15
 // alone in a loop), 8.5 for the plan.  The logits (16.8 MB) take 3.2 us at a copy's rate;
 // what bounds the choice is its 1300 vector instructions per four tokens, and at its end
 // the few tokens decided in fp64 (up to 4 us after the others).  16 tokens, 8 experts: one
-// launch, 4.7 us.
+// launch, 4.9 us.  64 tokens of the 256 experts: 9.9 us, 6.4 of them the choice, which is
+// one wave's chain of instructions from the load of a row to its weights.
 #include "fp8gg_layer_internal.h"
 
 namespace fp8gg {
@@ -700,7 +703,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
 // Up to kLonePairs pairs, what its registers hold, a single workgroup counts them all
 // itself: many workgroups that read the same few lines of counts wait 3 to 5 us for them
 // (route with plan, one workgroup against many: 6.4 and 10.7 us at 256 tokens, 8 experts,
-// k = 2; 13.7 and 14.8 us at 256 tokens, 256 experts in groups, k = 8).  Fewer workgroups
+// k = 2; 13.7 and 14.8 us at 256 tokens, 256 experts in groups, k = 8, with 16 lanes per
+// token).  Fewer workgroups
 // of more pairs beyond that are slower (1024 tokens, 256 experts: 16.9 us, and 19.3 with
 // 4096 pairs each; 4096 tokens, 8 experts: 12.6 and 14.0).
 constexpr int kPlaceGroups = 64;
@@ -906,7 +910,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackwardArgs a
 //                   16: 9.8 against 11.0; 64: 9.9 and 15.0; 200: 10.9 and 13.8
 //   1024 (4096)     16 tokens of 64 lanes per workgroup: 15.5 (17.6) against 16.6 (21.8)
 //   16384           16 lanes: 24.6, and 40.2 with 64
-// 344 experts: 16 tokens 11.3 against 19.4.  Up to 128 experts 16 lanes stay the better ones
+// 344 experts: 16 tokens 11.2 against 19.4.  One launch while T E is small: 128 experts,
+// sigmoid and bias, 64 tokens take 8.6 in one and 7.6 in two.  Up to 128 experts 16 lanes stay the better ones
 // where counts are handed on (4096 tokens, 128 experts: 12.8 and 14.2 with 64), and up to 64
 // experts everywhere.  Without a plan 4 tokens per workgroup up to 2048 (8.3 against 9.4).
 //

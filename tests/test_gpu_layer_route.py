@@ -148,7 +148,7 @@ def test_masks_and_infinities(F):
 @pytest.mark.parametrize("T,E,k", [(64, 60, 4), (65, 60, 4), (1000, 60, 4), (16384, 60, 4), (16385, 60, 4), (40000, 60, 4),
                                    (40000, 61, 9), (70000, 256, 16), (3000, 1000, 5)])
 def test_many_tokens(F, T, E, k):
-    """One to 256 workgroups of 64 tokens, then several passes per workgroup, and more
+    """One to 256 rows of counts, then several passes per workgroup, and more
     pairs per wave of the plan than its registers hold; compared with a sort on the GPU,
     the oracle being slow here."""
     g = torch.Generator(device="cuda").manual_seed(T)
