@@ -234,6 +234,8 @@ __device__ __forceinline__ uint32_t keep_groups_exactly(const RouteArgs& a, int 
 // n_group keys (one word of padding per group keeps the lanes that scan the groups on
 // different banks).  Only this wave touches it.  Up to eight lanes scan a group where there
 // are enough.  ARITH: the keys are fp32 sums, and a border too close is decided in fp64.
+// With group_top 2 a score is half the sum: the halves are exact, and no sum of two finite
+// keys leaves fp32 (biases of the type's lowest value would take a group out).
 template <int L, int V, bool ARITH>
 __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int64_t t, int l, int tok, float* lds,
                                                 const float (&key)[V]) {
@@ -274,8 +276,9 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int64_t t, i
     if (m1 > none<float>()) largest = fabsf(m1);
     if (m2 > none<float>()) largest = MaxK()(largest, fabsf(m2));
   }
+  const float part = a.group_top == 2 ? 0.5f : 1.0f;
   if (g < a.n_group) {
-    best[g] = a.group_top == 2 && m2 > none<float>() ? m1 + m2 : m1;
+    best[g] = a.group_top == 2 && m2 > none<float>() ? part * m1 + part * m2 : part * m1;
     second[g] = a.group_top == 2 && m2 > none<float>() ? m2 : m1;
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -298,7 +301,7 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, int64_t t, i
   uint32_t kept = groups_within<float, L>(a, l, tok, mine, rank);
   if constexpr (ARITH) {
     // is the first group dropped too close to the last one kept for fp32?
-    const float margin = margin_of(a, team_reduce<L>(largest, MaxK()));
+    const float margin = part * margin_of(a, team_reduce<L>(largest, MaxK()));
     if (__any(l < a.n_group && mine > none<float>() && rank == a.topk_group && gap <= margin)) {
       const float low = l < a.n_group ? second[l] : none<float>();
       kept = keep_groups_exactly<L>(a, l, tok, buf, low - margin_of(a, low), exact_key<L>(a, t, l, true));

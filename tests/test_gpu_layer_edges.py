@@ -1,0 +1,50 @@
+"""GPU tests of the layer operators at the edges of their ranges: values near the ends of
+fp32, rows and places that hold nothing, more work than one pass of a grid, and rows of
+the router that leave its usual path."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer as L
+from tests import layer_parity as P
+from tests.test_gpu_layer_route import check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def F():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    import fp8_rowwise_scaled_amd as F
+    F.load()
+    return F
+
+
+LOWEST = float(np.finfo(np.float32).min)
+
+
+@pytest.mark.parametrize("T,per", [(40, 4), (40, 40), (4200, 40)])     # 16 lanes per token, 64, 16 with several keys each
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_past_fp32(F, T, per, score):
+    """Sums of two keys that fp32 cannot hold: a bias of the type's lowest value takes no group
+    out, and sums above the largest value keep their order."""
+    print(f"case group sums T={T} per={per} {score}", flush=True)
+    rng = np.random.default_rng(per)
+    x = torch.from_numpy(rng.normal(0, 1, (T, 4 * per)).astype(np.float32))
+
+    def bias(**of):
+        b = rng.normal(0, 0.1, (4, per)).astype(np.float32)
+        for g, v in of.items():
+            b[int(g[1:]), :len(v)] = v
+        return torch.from_numpy(b.reshape(-1))
+    low = bias(g0=[LOWEST] * per, g2=[LOWEST] * per)
+    for keep in (1, 3, 4):
+        check(F, x, 12, low, score=score, n_group=4, topk_group=keep, group_top=2, label=f"lowest, keep {keep}")
+    high = bias(g1=[3e38, 0.5e38], g2=[3e38, 3e38], g3=[0.9e38, 3e38])
+    for keep in (1, 2, 3):
+        check(F, x, 4, high, score=score, n_group=4, topk_group=keep, group_top=2, label=f"large, keep {keep}")
+    check(F, x, 4, bias(g0=[-3e38] * per, g1=[-2e38] * per, g2=[-2.5e38] * per, g3=[-np.inf] * per), score=score, n_group=4,
+          topk_group=2, group_top=2, label="negative")
+    check(F, x, 4, bias(g1=[np.inf, np.inf], g3=[np.inf, np.inf]), score=score, n_group=4, topk_group=1, group_top=2,
+          label="infinite")
