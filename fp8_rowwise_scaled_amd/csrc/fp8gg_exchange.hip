@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(ExchangeArgs
     if (dots) {
 #pragma unroll
       for (int u = 0; u < kRowsAtOnce; ++u) {
-        dot[u] = wave_reduce(dot[u], AddF());
+        // a place left out has 0, also where d times the zeros in its y is NaN
+        dot[u] = row[u] >= 0 ? wave_reduce(dot[u], AddF()) : 0.f;
         if (lane == 0) part[slot][wave][u] = dot[u];
       }
       __syncthreads();

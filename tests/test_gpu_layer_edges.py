@@ -48,3 +48,24 @@ def test_group_sums_past_fp32(F, T, per, score):
           topk_group=2, group_top=2, label="negative")
     check(F, x, 4, bias(g1=[np.inf, np.inf], g3=[np.inf, np.inf]), score=score, n_group=4, topk_group=1, group_top=2,
           label="infinite")
+
+
+@pytest.mark.parametrize("k", [1, 2, 3])
+@pytest.mark.parametrize("N", [264, 2056, 4104, 8200])
+def test_left_out_places_have_no_weight_gradient(F, N, k):
+    """... whatever their token's gradient holds."""
+    print(f"case left out N={N} k={k}", flush=True)
+    T, R = 24, 24 * k
+    g = torch.Generator(device="cuda").manual_seed(N + k)
+    dout = torch.randn(T, N, generator=g, device="cuda").to(torch.bfloat16)
+    dout[3, N // 2], dout[4, 5], dout[5] = float("nan"), float("inf"), -float("inf")
+    y = torch.randn(R, N, generator=g, device="cuda").to(torch.bfloat16)
+    dst = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32).view(T, k)
+    out = torch.zeros((T, k), dtype=torch.bool, device="cuda")
+    out[::2, k - 1], out[3:6, 0] = True, True
+    dst[out] = torch.where(torch.arange(int(out.sum()), device="cuda") % 2 == 0, -1, R).to(torch.int32)
+    _, dw = F.f8f8bf16_moe_combine_backward(dout, dst, torch.ones(T, k, device="cuda"), y)
+    assert torch.all(dw[out] == 0), dw[out]
+    good = ~out
+    good[3:6] = False
+    assert torch.all(dw[good] != 0) and torch.all(torch.isfinite(dw[good]))
