@@ -82,15 +82,41 @@ __device__ __forceinline__ void load_row(const NormArgs& a, int64_t base, int la
   }
 }
 
+// Below this mean of squares (plus eps) the squares have left what fp32 holds in full: above
+// it those that underflow, by at most 2^-150 each, change the mean by less than 2^-50 of it.
+constexpr float kSmallMean = 0x1p-100f;
+
+// The mean of such a row's (h 2^96)^2, plus eps 2^192: the largest |h| is below 2^-42 (K <=
+// 2^15), so no square overflows, and the smallest bf16 value, 2^-133, has a square of 2^-74.
+// Such rows are rare: every wave reads all of h again, after the barrier of the team that
+// wrote it, and there is no second one.  The check costs the other rows about 1% (8 x 7168:
+// 3.60 -> 3.66 us; 1500 x 16384: 33.0 -> 33.3).
+__device__ __forceinline__ float mean_of_small(const NormArgs& a, int64_t base, int lane, float inv_k) {
+  const u32x4* rows = reinterpret_cast<const u32x4*>(a.residual ? a.residual_out : a.X) + base;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int j = lane & 63; j < a.K / 8; j += 64) {
+    const F8 h = unpack_bf16(rows[j]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(h.v[e] * 0x1p96f, h.v[e] * 0x1p96f, sum);
+  }
+  return __builtin_fmaf(wave_reduce(sum, AddF()), inv_k, a.eps * 0x1p96f * 0x1p96f);
+}
+
 template <int TPR, int NV, bool BLOCKED>
 __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_quantize_kernel(NormArgs a) {
   constexpr int kTeams = threads_of(TPR) / TPR;
-  const int lane = threadIdx.x % TPR;
   const int team = threadIdx.x / TPR;
   const int nvec = a.K / 8;
   const float inv_k = 1.0f / (float)a.K;
   int slot = 0;
   for (int64_t row = (int64_t)blockIdx.x * kTeams + team; row < a.rows; row += (int64_t)gridDim.x * kTeams) {
+    int lane = threadIdx.x % TPR;
+    // 1024 threads: opaque to the compiler in each row, or it keeps all addresses in registers
+    // across the rows, 78 with two vectors, and only one workgroup fits a CU (34.9 against
+    // 33.2 us at 1500 x 16384).  Not the smaller ones: their weights are then asked for
+    // later (8 x 7168: 3.76 against 3.66 us).
+    if constexpr (TPR == 1024) asm volatile("" : "+v"(lane));
     const int64_t base = row * nvec;
     u32x4 raw[NV], res[NV];
     if (a.stream) load_row<true, TPR>(a, base, lane, raw, res);
@@ -130,7 +156,13 @@ __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_quantize_kernel(NormA
     }
     team_reduce<TPR>(sum, most, slot);
     slot ^= 1;
-    const float rstd = 1.0f / sqrtf(__builtin_fmaf(sum, inv_k, a.eps));
+    float mean = __builtin_fmaf(sum, inv_k, a.eps), up = 1.0f;
+    if (mean < kSmallMean) {                         // the same for the whole team
+      mean = mean_of_small(a, base, lane, inv_k);
+      up = 0x1p96f;
+    }
+    // a row of zeros without eps: 0, so that neither its output nor its gradient is NaN
+    const float rstd = mean == 0.f ? 0.f : up / sqrtf(mean);
     if constexpr (BLOCKED) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {

@@ -53,10 +53,11 @@ typedef enum {
 
 /*
  * Root-mean-square norm with the residual's addition and an fp8 output (the scale's floor
- * is applied to h * weight, before rstd; h^2 has to be finite in fp32):
+ * is applied to h * weight, before rstd; h^2, h * weight and rstd have to be finite in
+ * fp32, so without eps a row's root mean square has to be above 2^-128):
  *
  *     h    = bf16_rne(X + residual)          (h = X without a residual)
- *     rstd = 1 / sqrt(mean_k h^2 + eps)
+ *     rstd = 1 / sqrt(mean_k h^2 + eps)   (0 for a row of zeros when eps is 0)
  *     y    = h * rstd * weight
  *     XQ, x_scale = codes and scales of y;   Y = bf16_rne(y)
  *

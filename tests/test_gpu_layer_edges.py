@@ -69,3 +69,42 @@ def test_left_out_places_have_no_weight_gradient(F, N, k):
     good = ~out
     good[3:6] = False
     assert torch.all(dw[good] != 0) and torch.all(torch.isfinite(dw[good]))
+
+
+@pytest.mark.parametrize("K", [256, 1024, 2048, 4096, 7168, 8192, 16384, 20480])
+@pytest.mark.parametrize("block", [0, 128])
+@pytest.mark.parametrize("eps", [0.0, 1e-38])
+def test_norm_of_rows_whose_squares_leave_fp32(F, K, block, eps):
+    """Rows down to 2^-90: their squares are below what fp32 holds, their norm is not.  A row of
+    zeros has rstd 0 without eps, so that neither it nor its gradient holds a NaN."""
+    print(f"case small rows K={K} block={block} eps={eps}", flush=True)
+    rng = np.random.default_rng(K)
+    powers = [0, -40, -48, -50, -60, -64, -70, -80, -90]
+    x = rng.normal(0, 1, (len(powers) + 1, K)) * 2.0 ** np.array(powers + [0], np.float64)[:, None]
+    x[-1] = 0.0
+    x = P.to_bf16(x)
+    res = torch.zeros_like(x)
+    w = torch.from_numpy(rng.normal(1, 0.3, K).astype(np.float32))
+    for residual in (None, res.cuda()):
+        # in place: the branch may not read a residual that has been overwritten
+        out = F.f8f8bf16_rmsnorm_quantize(x.cuda(), w.cuda(), eps, residual=residual, residual_out=residual, block=block,
+                                          want_y=True, want_rstd=True)
+        X, W, E = P.f64(x), P.f64(w), np.float64(np.float32(eps))
+        with np.errstate(divide="ignore", invalid="ignore"):
+            h, y, rstd = L.rmsnorm(X, None, W, E)
+        if eps == 0.0:
+            y[-1], rstd[-1] = 0.0, 0.0
+        P.assert_close(out.rstd, rstd, 2.0 ** -18 * rstd, "rstd")
+        P.assert_close(out.Y, y, (P.BF16 + 2.0 ** -18) * np.abs(y) + 1e-40, "Y")
+        hw = L.block_amax(X * W, block)
+        scale = np.where(hw > 0, np.maximum(hw, 2.0 ** -100) / 448 * (rstd if not block else rstd[:, None]), 1.0)
+        P.assert_close(out.x_scale, scale, 2.0 ** -18 * scale, "x_scale")
+        P.assert_codes(out.XQ, X * W / L.spread(L.scale_of(hw), K), 2.0 ** -21, "codes")
+    dy = P.to_bf16(rng.normal(0, 1, x.shape) * 1e-2)
+    dx, dw = F.f8f8bf16_rmsnorm_backward(dy.cuda(), x.cuda(), w.cuda(), out.rstd, res.cuda())
+    R, DY = P.f64(out.rstd), P.f64(dy)
+    want, want_w = L.rmsnorm_backward(DY, X, W, R, None)
+    xhat = X * R[:, None]
+    size = R[:, None] * (np.abs(DY * W) + np.abs(xhat) * np.abs(DY * W * xhat).mean(1, keepdims=True))
+    P.assert_close(dx, want, P.BF16 * np.abs(want) + 2.0 ** -18 * size + 1e-40, "dX")
+    P.assert_close(dw, want_w, (x.shape[0] + 48) * P.U * np.abs(DY * xhat).sum(0) + 1e-30, "dweight")
