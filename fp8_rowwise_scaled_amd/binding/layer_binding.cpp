@@ -288,6 +288,8 @@ PyObject* route(PyObject* const* args, Py_ssize_t n) {
   const at::Tensor* bias = c.tensor("bias", true);
   if (bias) c.check(*bias, "bias", at::kFloat, {E});
   const int64_t score = c.integer(), n_group = c.integer(), topk_group = c.integer(), group_top = c.integer();
+  // here, because the library takes an int
+  if (group_top != 1 && group_top != 2) refuse("group_top=%lld must be 1 or 2", (long long)group_top);
   const bool renormalize = c.flag();
   const double scale = c.number();
   const bool plan = c.flag();
@@ -349,6 +351,8 @@ int64_t rows_of(Call& c, int64_t T, int64_t k) {
   }
   const int64_t rows = c.integer();
   if (rows < 0) refuse("rows must not be negative, got %lld", (long long)rows);
+  // the library's bound, before anything of that size is allocated
+  if (rows > (int64_t(1) << 31) - 256) refuse("rows=%lld is too large", (long long)rows);
   return rows;
 }
 

@@ -108,3 +108,17 @@ def test_norm_of_rows_whose_squares_leave_fp32(F, K, block, eps):
     size = R[:, None] * (np.abs(DY * W) + np.abs(xhat) * np.abs(DY * W * xhat).mean(1, keepdims=True))
     P.assert_close(dx, want, P.BF16 * np.abs(want) + 2.0 ** -18 * size + 1e-40, "dX")
     P.assert_close(dw, want_w, (x.shape[0] + 48) * P.U * np.abs(DY * xhat).sum(0) + 1e-30, "dweight")
+
+
+def test_integers_are_not_cut(F):
+    """Integers past 32 bits are refused, not taken for their low half."""
+    x = torch.randn(8, 32, device="cuda")
+    dst = torch.zeros((8, 1), dtype=torch.int32, device="cuda")
+    q, s = torch.zeros((8, 32), dtype=torch.uint8, device="cuda"), torch.ones(8, device="cuda")
+    for call, text in [(lambda: F.f8f8bf16_route(x, 2, n_group=4, topk_group=2, group_top=2 ** 32 + 2), "group_top"),
+                       (lambda: F.f8f8bf16_route(x, 2, group_top=1 - 2 ** 32), "group_top"),
+                       (lambda: F.f8f8bf16_rmsnorm_quantize(x.to(torch.bfloat16), s.new_ones(32), block=2 ** 32), "block"),
+                       (lambda: F.f8f8bf16_moe_dispatch(q, s, dst, rows=2 ** 40), "too large"),
+                       (lambda: F.f8f8bf16_moe_combine_backward(x.to(torch.bfloat16), dst, rows=2 ** 40), "too large")]:
+        with pytest.raises(ValueError, match=text):
+            call()
