@@ -68,11 +68,14 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(DispatchArgs a, Spli
       if (v < nvec) store_out(reinterpret_cast<u32x4*>(a.XQs) + r * nvec + v, x);
     }
     if (c == 0) {
-      for (int s = threadIdx.x; s < a.scale_cols; s += split.threads) {
-        const float scale = a.x_scale[t * a.scale_cols + s];
+      // in whole waves: the places are read from lanes that may have no scale of their own
+      for (int s0 = 0; s0 < a.scale_cols; s0 += split.threads) {
+        const int s = s0 + threadIdx.x;
+        float scale = 0.f;
+        if (s < a.scale_cols) scale = a.x_scale[t * a.scale_cols + s];
         for (int j = 0; j < a.k; ++j) {
           const int64_t r = row_of(p, j);
-          if (r >= 0 && r < a.R) a.xs_out[r * a.scale_cols + s] = scale;
+          if (s < a.scale_cols && r >= 0 && r < a.R) a.xs_out[r * a.scale_cols + s] = scale;
         }
       }
     }

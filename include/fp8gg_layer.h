@@ -157,7 +157,7 @@ fp8gg_status f8f8bf16_route_backward(
  *   x_scale  [T, scale_cols]   fp32         xs_out  [R, scale_cols]
  *   dst_row  [T, k]            int32
  *
- * K % 16 == 0, k <= 64; XQ and XQs 16-byte aligned.
+ * K % 16 == 0, 1 <= scale_cols <= K, k <= 64; XQ and XQs 16-byte aligned.
  */
 fp8gg_status f8f8bf16_moe_dispatch(
     const uint8_t* XQ, const float* x_scale, int64_t scale_cols, const int32_t* dst_row, uint8_t* XQs, float* xs_out,

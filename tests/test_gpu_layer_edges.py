@@ -122,3 +122,24 @@ def test_integers_are_not_cut(F):
                        (lambda: F.f8f8bf16_moe_combine_backward(x.to(torch.bfloat16), dst, rows=2 ** 40), "too large")]:
         with pytest.raises(ValueError, match=text):
             call()
+
+
+@pytest.mark.parametrize("T,k,K,cols", [(5, 8, 64, 3), (9, 64, 512, 65), (3, 40, 304, 300), (4, 33, 4096, 256), (2, 3, 8192, 500)])
+def test_dispatch_of_any_number_of_scales(F, T, k, K, cols):
+    """Fewer scales than a wave has lanes, more than a workgroup, and places in lanes without one."""
+    print(f"case dispatch scales T={T} k={k} K={K} cols={cols}", flush=True)
+    rng = np.random.default_rng(T + cols)
+    R = T * k + 1
+    dst = rng.permutation(R)[:T * k].reshape(T, k)
+    dst[0, k - 1] = -1
+    q, s = rng.integers(0, 256, (T, K), dtype=np.uint8), rng.random((T, cols)).astype(np.float32)
+    oq, os_ = P.Guarded((R, K), torch.uint8), P.Guarded((R, cols), torch.float32)
+    F.f8f8bf16_moe_dispatch(torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), torch.from_numpy(dst.astype(np.int32)).cuda(),
+                            rows=R, XQs=oq.t, xs_out=os_.t)
+    torch.cuda.synchronize()
+    oq.check()
+    os_.check()
+    for got, rows in ((oq, q), (os_, s)):
+        want, written = L.dispatch(rows, dst, R)
+        assert np.array_equal(got.t.cpu().numpy()[written], want[written])
+        assert np.all(got.untouched(~written))
