@@ -74,8 +74,9 @@ def link_binding(obj: str) -> str:
 
 
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile every source under csrc/ and the binding; link libfp8gg.so and
-    _layer_binding.so.  Always rebuilds."""
+    """Compile every source under csrc/ and the binding; link libfp8gg.so, then
+    _layer_binding.so.  Always rebuilds.  The library needs hipcc alone: it is built also
+    where the binding (torch, Python's headers, g++) cannot be, which raises after it."""
     hipcc = _hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
@@ -97,14 +98,17 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     with ThreadPoolExecutor(max(1, min(8, len(srcs) + 1))) as ex:
         binding = ex.submit(compile_binding, binding_obj)
         list(ex.map(compile_one, zip(srcs, objs)))
-        binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB)
-    link_binding(binding_obj)
+    try:
+        binding.result()
+        link_binding(binding_obj)
+    except Exception as e:
+        raise RuntimeError(f"{LIB} is built, the binding of the layer operators is not: {e}") from e
     if verbose:
         print(f"built {LIB} and {BINDING}")
     return LIB
