@@ -68,9 +68,6 @@ LAYER_EXPORTS = (
     "f8f8bf16_layer_last_error",
 )
 
-DTYPE_BF16 = 0
-DTYPE_F32 = 1
-DTYPE_E4M3 = 2
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
 
@@ -181,15 +178,6 @@ def check(status: int, what: str) -> None:
 
 def layer_last_error() -> str:
     return load().f8f8bf16_layer_last_error().decode()
-
-
-def layer_check(status: int, what: str) -> None:
-    if status == OK:
-        return
-    msg = f"{what}: {layer_last_error()}"
-    if status in (ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED_SHAPE):
-        raise ValueError(msg)
-    raise RuntimeError(msg)
 
 
 def plan(layout: int, preshuffled: bool, G: int, M: int, N: int, K: int) -> dict:
