@@ -143,3 +143,108 @@ def test_dispatch_of_any_number_of_scales(F, T, k, K, cols):
         want, written = L.dispatch(rows, dst, R)
         assert np.array_equal(got.t.cpu().numpy()[written], want[written])
         assert np.all(got.untouched(~written))
+
+
+@pytest.mark.parametrize("T", [90, 4200])                              # 64 and 16 lanes per token
+@pytest.mark.parametrize("E", [256, 344])
+@pytest.mark.parametrize("kind", ["equal", "padded", "random"])
+@pytest.mark.parametrize("score,biased,groups", [("softmax", False, False), ("softmax", True, False), ("sigmoid", True, True),
+                                                 ("sigmoid", False, True)])
+def test_rows_with_many_candidates(F, T, E, kind, score, biased, groups):
+    """More keys than the list of candidates holds: rows of equal logits (all, or every fourth as
+    padding leaves them) and k = 16; with and without sums that fp32 cannot tell apart."""
+    print(f"case candidates T={T} E={E} {kind} {score} bias={biased} groups={groups}", flush=True)
+    rng = np.random.default_rng(T + E)
+    x = rng.normal(0, 1, (T, E)).astype(np.float32)
+    if kind == "equal":
+        x[:] = 0.0
+    elif kind == "padded":
+        x[3::4] = 0.25
+    b = (rng.integers(0, 3, E) * 2.0 ** -30).astype(np.float32) if biased else None
+    kw = dict(n_group=8, topk_group=4, group_top=2) if groups else {}
+    check(F, torch.from_numpy(x), 16 if kind == "random" else 8, None if b is None else torch.from_numpy(b), score=score, **kw)
+
+
+def test_weights_of_softmax_with_a_bias_and_bf16_sigmoid(F):
+    """What crosses to fp64 most often: keys of many small shares, and bf16 logits that tie."""
+    rng = np.random.default_rng(31)
+    x = torch.from_numpy(rng.normal(0, 0.5, (4200, 256)).astype(np.float32))
+    b = torch.from_numpy(rng.normal(0, 1e-3, 256).astype(np.float32))
+    check(F, x, 8, b, score="softmax")
+    check(F, x.to(torch.bfloat16), 8, torch.zeros(256), score="sigmoid")
+
+
+def places(T, k, seed):
+    """A permutation of the T k rows, a tenth of the places left out."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dst = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32).view(T, k)
+    dst[torch.rand((T, k), generator=g, device="cuda") < 0.1] = -1
+    return g, dst
+
+
+@pytest.mark.parametrize("T,k,N", [(1_100_000, 1, 8), (1_100_000, 1, 264), (700_000, 3, 16), (1_100_000, 2, 40)])
+def test_exchange_of_more_tokens_than_a_grid_has_workgroups(F, T, k, N):
+    """A workgroup takes several tokens: 2^20 of them are the most that one launch has."""
+    print(f"case exchange T={T} k={k} N={N}", flush=True)
+    g, dst = places(T, k, T + N)
+    y = torch.randn(T * k, N, generator=g, device="cuda").to(torch.bfloat16)
+    # small whole weights and gradients: sums and products are exact in fp32, whatever their order
+    w = torch.randint(-4, 5, (T, k), generator=g, device="cuda").float()
+    dout = torch.randint(-2, 3, (T, N), generator=g, device="cuda").to(torch.bfloat16)
+    y = (y * 4).round() / 4
+    here = dst >= 0
+    at = dst.long().clamp(min=0)
+    rows = torch.where(here[:, :, None], y[at].float(), 0.0)
+    out = F.f8f8bf16_moe_combine(y, dst, w)
+    assert torch.equal(out, (rows * w[:, :, None]).sum(1).to(torch.bfloat16))
+    mark = torch.full_like(y, 7.0)
+    dy, dw = F.f8f8bf16_moe_combine_backward(dout, dst, w, y, dY=mark)
+    assert torch.equal(dw, (rows * dout.float()[:, None]).sum(2))
+    want = torch.full_like(y, 7.0)
+    want[at[here]] = (dout.float()[:, None] * w[:, :, None]).to(torch.bfloat16)[here]
+    assert torch.equal(dy, want)
+
+
+def test_dispatch_of_more_tokens_than_a_grid_has_workgroups(F):
+    T, k, K = 1_100_000, 2, 16
+    g, dst = places(T, k, 5)
+    q = torch.randint(0, 256, (T, K), dtype=torch.uint8, generator=g, device="cuda")
+    s = torch.rand(T, generator=g, device="cuda")
+    out, scales = torch.full((T * k, K), 9, dtype=torch.uint8, device="cuda"), torch.full((T * k,), 9.0, device="cuda")
+    want, want_s = out.clone(), scales.clone()
+    F.f8f8bf16_moe_dispatch(q, s, dst, XQs=out, xs_out=scales)
+    here = dst >= 0
+    token = torch.arange(T, device="cuda")[:, None].expand(T, k)[here]
+    want[dst[here].long()], want_s[dst[here].long()] = q[token], s[token]
+    assert torch.equal(out, want) and torch.equal(scales, want_s)
+
+
+def test_activation_of_more_rows_than_a_grid_has_workgroups(F):
+    """... compared with the same rows in smaller calls."""
+    rows, I = 4_300_000, 8
+    g = torch.Generator(device="cuda").manual_seed(6)
+    h = torch.randn(rows, 2 * I, generator=g, device="cuda").to(torch.bfloat16)
+    da = torch.randn(rows, I, generator=g, device="cuda").to(torch.bfloat16)
+    a = F.f8f8bf16_silu_mul_quantize(h, checkpoint=True)
+    d = F.f8f8bf16_silu_mul_backward(da, a.HQ, a.h_scale)
+    for start in (0, 262_144, 2_000_000, 4_194_300, 4_250_000):
+        part = slice(start, start + 50_000)
+        b = F.f8f8bf16_silu_mul_quantize(h[part], checkpoint=True)
+        assert all(torch.equal(x[part], y) for x, y in zip(a, b))
+        assert torch.equal(d[part], F.f8f8bf16_silu_mul_backward(da[part], b.HQ, b.h_scale))
+
+
+@pytest.mark.parametrize("rows,K", [(70_000, 1032), (300_000, 264), (70_000, 2056)])
+@pytest.mark.parametrize("block", [0, 128])
+def test_norm_of_more_rows_than_a_grid_has_teams(F, rows, K, block):
+    """The sums of a team's second row use the other half of its exchange buffer."""
+    K = K // 128 * 128 if block else K
+    print(f"case norm rows={rows} K={K} block={block}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, K, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.rand(K, generator=g, device="cuda") + 0.5
+    a = F.f8f8bf16_rmsnorm_quantize(x, w, block=block, want_rstd=True)
+    for start in (0, 60_000, 65_530, rows - 4000):
+        part = slice(start, start + 4000)
+        b = F.f8f8bf16_rmsnorm_quantize(x[part], w, block=block, want_rstd=True)
+        assert torch.equal(a.XQ[part], b.XQ) and torch.equal(a.x_scale[part], b.x_scale) and torch.equal(a.rstd[part], b.rstd)
