@@ -8,12 +8,12 @@
 // third of the instructions of k rounds of a maximum over the team (48 us at 16384
 // tokens, 256 experts in 8 groups, k = 8, against 18).
 //
-// What has to be compared exactly.  Scores rise with their logits, so without a bias
-// and with groups ranked by their best expert the logits themselves are the keys: exact
-// and no exponential.  Otherwise keys are p + bias or sums of two of them in fp32, off
-// by a few units in the last place; where two of the ranked keys (or the last group kept
-// and the first one dropped) are nearer than the error bound, those keys are computed
-// again in fp64 and ranked by that.
+// What has to be compared exactly.  Scores rise with their logits, so without a bias the
+// logits themselves rank the experts, and the groups where their best expert stands for
+// them: exact and no exponential.  Otherwise keys are p + bias or sums of two of them in
+// fp32, off by a few units in the last place; where two of the ranked keys (or the last
+// group kept and the first one dropped) are nearer than the error bound, those keys are
+// computed again in fp64 and ranked by that.
 //
 // Plan.  A stable counting sort of the pairs by expert: each workgroup counts its
 // tokens' experts, the second kernel adds up the counts before its own block and ranks
@@ -132,9 +132,8 @@ __device__ __forceinline__ K margin_of(const RouteArgs& a, K s) {
 }
 
 // The key of one expert in fp64, from its logit in memory (taken seldom, so nothing is
-// kept in registers for it).  Keys are multiples of 2^-44: sums of two scores that are
-// equal in exact arithmetic, as sigmoid(x) + sigmoid(-x) for every x, then tie, and
-// adding two such keys rounds nothing more.  Bare scores: the logit itself.
+// kept in registers for it).  Not rounded further: scores far below the row's largest, and
+// sigmoids near 1, keep their order.  Without arith: the logit itself.
 //
 // A call, not inlined: the polynomials of exp would otherwise be kept in registers
 // through the whole kernel and push its own values out.
@@ -151,7 +150,7 @@ struct ExactKey {
     const double b = a.bias ? (double)counted(a.bias[e]) : 0.0;
     const double w = exact_exp(a.sigmoid ? -x : x - most);
     const double p = a.sigmoid ? 1.0 / (1.0 + w) : w / sum;
-    return x > none<double>() && b > none<double>() ? rint((p + b) * 0x1p44) * 0x1p-44 : none<double>();
+    return x > none<double>() && b > none<double>() ? p + b : none<double>();
   }
 };
 
@@ -180,6 +179,13 @@ struct GroupOf {
 };
 
 constexpr int kMaxGroups = 16;
+
+// x to 44 significant bits (halves away from zero): sums of two keys that are equal in exact
+// arithmetic, as sigmoid(x) + sigmoid(-x) for every x, are the same then, whatever their
+// last bits in fp64.
+__device__ __forceinline__ double significant(double x) {
+  return __builtin_bit_cast(double, (__builtin_bit_cast(uint64_t, x) + 0x100) & ~uint64_t(0x1FF));
+}
 
 // The groups kept, as a mask, from lane g's (g < n_group) score and its rank.
 template <typename K, int L>
@@ -221,7 +227,7 @@ __device__ __forceinline__ uint32_t keep_groups_exactly(const RouteArgs& a, int 
     for (int i = 0; i < per; ++i)
       if (own[i] >= least) take(key(l * per + i));
   }
-  if (a.group_top == 2 && m2 > none<double>()) m1 += m2;
+  if (a.group_top == 2 && m1 > none<double>()) m1 = significant(m2 > none<double>() ? m1 + m2 : m1);
   int rank = 0;
   for (int o = 0; o < a.n_group; ++o) {
     const double other = __shfl(m1, (L == 64 ? 0 : tok * L) + o, 64);
@@ -616,20 +622,27 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
     }
     if (a.n_group > 1) {
       kept = keep_groups<L, V, ARITH>(a, t, l, tok, reinterpret_cast<float*>(own_lds), key);
+      if (ARITH && !a.bias) {                        // the experts themselves in order of their logits
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = x[v];
+      }
       drop_groups<L, V>(a, l, kept, key);
     }
     const float bound = bound_of<L, V>(a.k, key);
-    const int n = gather<L, V>(a, l, ARITH ? bound - margin_of(a, bound) : bound, key, list);
+    const bool sums = ARITH && a.bias;
+    const int n = gather<L, V>(a, l, sums ? bound - margin_of(a, bound) : bound, key, list);
     const int listed = n < kCandidates ? n : kCandidates;
     bool near = false;
-    rank<L, ARITH>(a, l, listed, list, near);
-    if constexpr (ARITH) {
+    if (sums) {
+      rank<L, true>(a, l, listed, list, near);
       if (__any(near && n <= kCandidates)) rank_exactly<L>(a, l, listed, list, exact_key<L>(a, t, l, true));
+    } else {
+      rank<L, false>(a, l, listed, list, near);
     }
     int id = -1;
     if (l < a.k) id = list.chosen[l];
     if (__any(n > kCandidates)) {
-      const int in_rounds = choose_in_rounds<L>(a, l, kept, exact_key<L>(a, t, l, ARITH));
+      const int in_rounds = choose_in_rounds<L>(a, l, kept, exact_key<L>(a, t, l, sums));
       if (n > kCandidates) id = in_rounds;
     }
     // Weights: lane j has the j-th expert; all of them lie in the team's first 16 lanes.

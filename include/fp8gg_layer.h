@@ -112,9 +112,10 @@ int64_t f8f8bf16_rmsnorm_backward_workspace(int64_t rows, int64_t K);
  *     chosen = the k highest keys, descending; ties go to the lowest index
  *     weight = scale * p / (sum of the chosen p)     (renormalize)   or   scale * p
  *
- * The choice is that of exact arithmetic on the given logits and bias with keys rounded
- * to multiples of 2^-44 (bare scores: in the order of their logits); where fp32 cannot
- * tell two keys or group scores apart the row is decided in fp64.
+ * The choice is that of exact arithmetic on the given logits and bias, as far as fp64
+ * tells: without a bias experts rank by their logits, else by their keys in fp64 (a score
+ * below 2^-53 of its bias does not count); a group's sum of two keys is rounded to 44
+ * significant bits, so that sums which are equal, as sigmoid(x) + sigmoid(-x) = 1, tie.
  * A logit or bias of -infinity or NaN takes its expert out; +infinity counts as the
  * largest finite fp32.  A group without an expert left is never kept.  Slots for which
  * no expert is left hold id -1, weight 0 and dst_row -1, as in a row whose logits are

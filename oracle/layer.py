@@ -85,25 +85,31 @@ def shares(x, score):
     return w / w.sum()
 
 
+def significant(x, bits=44):
+    """x rounded to so many significant bits, halves away from zero."""
+    m, e = np.frexp(np.float64(x))
+    return float(np.ldexp(np.trunc(m * 2.0 ** bits + np.copysign(0.5, m)), e - bits))
+
+
 def route(logits, k, bias=None, score="softmax", n_group=1, topk_group=1, group_top=1, renormalize=True, scale=1.0):
     """(weights, ids): one token after the other, by sorting."""
     x = _counted(np.asarray(logits, np.float64))
     T, E = x.shape
     b = np.zeros(E) if bias is None else _counted(np.asarray(bias, np.float64))
     p = scores(x, score)
-    exact_order = bias is None and (n_group == 1 or group_top == 1)   # p rises with x
     weights, ids = np.zeros((T, k)), np.full((T, k), -1, np.int64)
     per = E // n_group
     for t in range(T):
         ok = (x[t] > -np.inf) & (b > -np.inf)
-        # on a grid of 2^-44, so that sums which are equal in exact arithmetic tie
-        key = np.where(ok, x[t] if exact_order else np.round((p[t] + b) * 2.0 ** 44) / 2.0 ** 44, -np.inf)
+        sums = np.where(ok, p[t] + b, -np.inf)
+        key = np.where(ok, x[t], -np.inf) if bias is None else sums       # p rises with x
         if n_group > 1:
             best = []
             for g in range(n_group):
-                v = np.sort(key[g * per:(g + 1) * per])[::-1][:group_top]
+                v = np.sort((key if group_top == 1 else sums)[g * per:(g + 1) * per])[::-1][:group_top]
                 v = v[v > -np.inf]
-                best.append(v.sum() if v.size else -np.inf)
+                # sums that are equal in exact arithmetic tie
+                best.append(-np.inf if not v.size else v[0] if group_top == 1 else significant(v.sum()))
             order = sorted(range(n_group), key=lambda g: (-best[g], g))
             kept = [g for g in order[:topk_group] if best[g] > -np.inf]
             key = np.where(np.isin(np.arange(E) // per, kept), key, -np.inf)

@@ -248,3 +248,25 @@ def test_norm_of_more_rows_than_a_grid_has_teams(F, rows, K, block):
         part = slice(start, start + 4000)
         b = F.f8f8bf16_rmsnorm_quantize(x[part], w, block=block, want_rstd=True)
         assert torch.equal(a.XQ[part], b.XQ) and torch.equal(a.x_scale[part], b.x_scale) and torch.equal(a.rstd[part], b.rstd)
+
+
+@pytest.mark.parametrize("T,E", [(90, 64), (90, 256), (4200, 256)])
+@pytest.mark.parametrize("zero_bias", [False, True])
+@pytest.mark.parametrize("group_top", [0, 1, 2])
+def test_scores_far_below_the_largest(F, T, E, zero_bias, group_top):
+    """Experts and groups are told apart by scores far below the row's largest, and by how far
+    sigmoids are from 1: exact arithmetic does, and fp64 where the scores are small."""
+    print(f"case small scores T={T} E={E} zero bias={zero_bias} group_top={group_top}", flush=True)
+    rng = np.random.default_rng(E + T)
+    b = torch.zeros(E) if zero_bias else None
+    kw = dict(n_group=8, topk_group=4, group_top=group_top) if group_top else {}
+    peaked = rng.normal(0, 12, (T, E))
+    peaked[::3, rng.integers(0, E)] += 60.0
+    check(F, torch.from_numpy(peaked.astype(np.float32)), 8, b, score="softmax", label="peaked", **kw)
+    # shares below fp32's range: the plain weights are 0 there, the choice is not open
+    far = rng.normal(-60, 10, (T, E))
+    far[:, 3] = 90.0
+    check(F, torch.from_numpy(far.astype(np.float32)), 8, b, score="softmax", label="far", **kw)
+    check(F, torch.from_numpy(rng.normal(-45, 4, (T, E)).astype(np.float32)), 8, b, score="sigmoid", label="low", **kw)
+    near_one = rng.uniform(14, 20, (T, E)).astype(np.float32)
+    check(F, torch.from_numpy(near_one), 8, b, score="sigmoid", label="near one", **kw)
