@@ -61,6 +61,14 @@ const char* name_of(at::ScalarType t) {
   }
 }
 
+// The interpreter's lock given up for a scope, however it is left.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // One call's arguments: a cursor over them, the first tensor's device, and the outputs.
 class Call {
  public:
@@ -145,13 +153,16 @@ class Call {
   }
 
   // Makes the library's call on the tensors' device and its current stream, without the
-  // interpreter's lock.  The call throws nothing.
+  // interpreter's lock.  The library throws nothing, but a tensor that has no memory (one of
+  // a tracer's) throws when it is asked for its address.
   template <typename Library>
   void run(Library library) const {
     void* stream = c10::hip::getCurrentHIPStream(device_.index()).stream();
-    PyThreadState* lock = PyEval_SaveThread();
-    const fp8gg_status st = library(stream);
-    PyEval_RestoreThread(lock);
+    fp8gg_status st;
+    {
+      const Unlocked unlocked;
+      st = library(stream);
+    }
     if (st == FP8GG_OK) return;
     const std::string what = std::string(name_) + ": " + f8f8bf16_layer_last_error();
     if (st == FP8GG_ERR_HIP) throw std::runtime_error(what);

@@ -270,3 +270,18 @@ def test_scores_far_below_the_largest(F, T, E, zero_bias, group_top):
     check(F, torch.from_numpy(rng.normal(-45, 4, (T, E)).astype(np.float32)), 8, b, score="sigmoid", label="low", **kw)
     near_one = rng.uniform(14, 20, (T, E)).astype(np.float32)
     check(F, torch.from_numpy(near_one), 8, b, score="sigmoid", label="near one", **kw)
+
+
+def test_tensors_without_memory_are_refused(F):
+    """A tracer's stand-in for a GPU tensor throws when it is asked for its address: a Python error,
+    raised with the interpreter's lock held."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    x = torch.randn(8, 32, device="cuda")
+    F.f8f8bf16_route(x, 2)
+    with FakeTensorMode() as mode:
+        fake = mode.from_tensor(x)
+        for _ in range(3):
+            with pytest.raises(Exception):
+                F.f8f8bf16_route(fake, 2)
+    r = F.f8f8bf16_route(x, 2)
+    assert torch.equal(r.ids.long(), torch.sort(x, dim=1, descending=True, stable=True).indices[:, :2])
