@@ -16,6 +16,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -138,8 +139,12 @@ class Call {
   // A new tensor straight from torch's GPU allocator, on the current device (which place()
   // has set): 0.2 us, where at::empty's way through the dispatcher takes 0.7.
   at::Tensor fresh(at::ScalarType type, Shape shape) {
-    static c10::Allocator* const allocator =
-        at::empty({1}, at::TensorOptions().dtype(at::kByte).device(device_)).storage().allocator();
+    static c10::Allocator* const allocator = [this] {
+      // past the dispatcher's Python modes: one of them (a tracer's) may be on in the first call
+      const c10::impl::ExcludeDispatchKeyGuard no_modes(
+          c10::DispatchKeySet({c10::DispatchKey::Python, c10::DispatchKey::PythonTLSSnapshot}));
+      return at::empty({1}, at::TensorOptions().dtype(at::kByte).device(device_)).storage().allocator();
+    }();
     return at::Tensor(at::detail::empty_generic(c10::IntArrayRef(shape.begin(), shape.size()), allocator,
                                                 c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
   }

@@ -285,3 +285,30 @@ def test_tensors_without_memory_are_refused(F):
                 F.f8f8bf16_route(fake, 2)
     r = F.f8f8bf16_route(x, 2)
     assert torch.equal(r.ids.long(), torch.sort(x, dim=1, descending=True, stable=True).indices[:, :2])
+
+
+FIRST_CALL = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+import fp8_rowwise_scaled_amd as F
+x = torch.randn(8, 32, device="cuda")
+with FakeTensorMode() as mode:
+    fake = mode.from_tensor(x)
+    try:
+        F.f8f8bf16_route(fake, 2)
+    except Exception as e:
+        print("refused:", e)
+r = F.f8f8bf16_route(x, 2)
+assert torch.equal(r.ids.long(), torch.sort(x, dim=1, descending=True, stable=True).indices[:, :2])
+print("right")
+"""
+
+
+def test_a_first_call_under_a_tracer_leaves_no_trace():
+    """The GPU allocator that the binding keeps is torch's, whatever mode the first call ran in."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "refused" in r.stdout and r.stdout.strip().endswith("right"), r.stdout + r.stderr[-2000:]
