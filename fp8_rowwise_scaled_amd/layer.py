@@ -115,7 +115,8 @@ def f8f8bf16_moe_combine_backward(dout, dst_row, weights=None, Y=None, rows=None
     """Gradients of combine: dout [T, N] bf16, Y [R, N] the forward's rows (None: no
     gradient of the weights, and rows gives R, T * k by default).  Returns (dY [R, N]
     bf16, dweights float32 [T, k] or None); rows of dY that no entry of dst_row names are
-    not written.  With weights and Y None it is a dispatch of bf16 rows."""
+    not written, and two entries must not name the same row.  With weights and Y None it is
+    a dispatch of bf16 rows."""
     return _binding().moe_combine_backward(dout, dst_row, weights, Y, rows, dY, dweights)
 
 

@@ -20,7 +20,8 @@
  *     even; the values are fp32 before that one rounding.  The floor keeps 448 / amax
  *     finite; it is far below what activations and gradients hold.  fp32 arithmetic may
  *     place a value that lies within about 2^-21 of the midpoint of two codes on either
- *     side.  The sign of a zero code is unspecified.
+ *     side (an activation of silu_mul_quantize with gate g: (|g| + 4) 2^-22).  The sign of a
+ *     zero code is unspecified.
  *   - Inputs are expected finite.  A NaN or infinity makes the values that depend on it
  *     unspecified (its row; its scale block; its group's column) and no others.
  *   - Sums, norms, softmax statistics and dot products are held in fp32 or more.
@@ -185,8 +186,10 @@ fp8gg_status f8f8bf16_moe_combine(
  * The gradients of combine:
  *     dY[dst_row[t, j]] = bf16_rne(weights[t, j] * dout[t])
  *     dweights[t, j]    = sum_n dout[t, n] * Y[dst_row[t, j], n]     (0 where dst_row is left out)
- * Rows of dY that no entry names are not written.  weights NULL: ones.  Y and dweights
- * may both be NULL: then it is a dispatch of bf16 rows.  dY may be Y itself.
+ * Two entries must not name the same row (combine itself allows it): one of their
+ * gradients would be lost.  Rows of dY that no entry names are not written.  weights NULL:
+ * ones.  Y and dweights may both be NULL: then it is a dispatch of bf16 rows.  dY may be Y
+ * itself.
  */
 fp8gg_status f8f8bf16_moe_combine_backward(
     const uint16_t* dout, const int32_t* dst_row, const float* weights, const uint16_t* Y, uint16_t* dY,
@@ -199,6 +202,9 @@ fp8gg_status f8f8bf16_moe_combine_backward(
  *     AQ, a_scale = codes and scales of a
  *     HQ, h_scale = codes and scales of H, one scale per row, half and 128 columns
  *                   (the last block of a half may be shorter)
+ *
+ * a has to be finite in fp32.  A sigmoid below 2^-126 (gates below -87) may count as 0, here
+ * and in the gradient.
  *
  *   H        [rows, 2 I]   bf16
  *   AQ       [rows, I]     e4m3fn      a_scale  [rows] (block 0) or [rows, I / 128] (block 128)  fp32

@@ -312,3 +312,20 @@ def test_a_first_call_under_a_tracer_leaves_no_trace():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=100)
     assert r.returncode == 0 and "refused" in r.stdout and r.stdout.strip().endswith("right"), r.stdout + r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("block", [0, 128])
+def test_activations_of_gates_far_below_zero(F, block):
+    """What the header says of them: codes within (|g| + 4) 2^-22 and half a step, scales too."""
+    rng = np.random.default_rng(41)
+    tops = np.arange(0, -86, -5)
+    gate = tops[:, None] - rng.uniform(0, 1, (len(tops), 256))
+    up = rng.normal(0, 1, gate.shape) * 2.0 ** 60
+    h = P.to_bf16(np.concatenate([gate, up], axis=1))
+    out = F.f8f8bf16_silu_mul_quantize(h.cuda(), block=block)
+    a = L.silu_mul(P.f64(h))
+    scale = L.scale_of(L.block_amax(a, block))
+    for i, top in enumerate(tops):
+        rel = (abs(top) + 1 + 4) * 2.0 ** -22
+        P.assert_close(out.a_scale[i], scale[i], rel * scale[i], f"scale at {top}")
+        P.assert_codes(out.AQ[i:i + 1], (a / L.spread(scale, 256))[i:i + 1], rel, f"codes at {top}")
