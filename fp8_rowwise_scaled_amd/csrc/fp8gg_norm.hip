@@ -13,10 +13,11 @@
 // us, 6.1 TB/s (a copy of 1 GiB reaches 5.2); counters show each byte moved once.  8 x
 // 7168: 3.9 us, the latency of a load, two reductions and a launch.
 //
-// Backward.  Each team of threads walks rows team, team + parts, ...: one pass gathers
-// mean(w dY xhat), the row (still in registers) gives dX, and every thread keeps the
-// sum of dY xhat of its own columns in fp32 over all its rows.  The teams' sums go to
-// the workspace and a second kernel adds them in a fixed order.  4093 x 7184 with the
+// Backward.  Each team of threads walks every n-th row, n being the launch's teams: one pass
+// gathers mean(w dY xhat), the row (still in registers up to K = 16384) gives dX, and every
+// thread keeps the sum of dY xhat of its own columns in fp32 over all its rows.  A
+// workgroup's teams join their sums, which go to the workspace, one row per workgroup, and a
+// second kernel adds those in a fixed order.  4093 x 7184 with the
 // residual's gradient: 46 us, 5.1 TB/s, and 5 us for the 256 partial sums.  Loads past the
 // caches do not help here (55.2 against 54.1 us).
 #include "fp8gg_layer_internal.h"
@@ -214,8 +215,9 @@ __device__ __forceinline__ BackVec load_back(const NormBackwardArgs& a, int64_t 
 // in small workgroups): the weights, and the next row, which is asked for before this one
 // is reduced (1024 threads and 256 teams so, against 256 threads, four vectors and 512
 // teams without: 54.4 -> 51.8 us at 4093 x 7184).  Two vectors of 1024 threads: the row.
-// Four: nothing, the second pass over the row reads it again (kept, it went through
-// scratch memory: 130 us at 1228 x 20480).
+// Four: nothing, the second pass over the row reads it again: 65 us at 1228 x 20480, 3.1 TB/s
+// of what the call cannot do without (with the row kept, in scratch memory, 130).  Its sums of
+// dweight alone take 32 of the 128 registers; 48 bytes per thread still go through scratch.
 template <int TPR, int NV>
 __global__ void __launch_bounds__(threads_of(TPR)) rmsnorm_backward_kernel(NormBackwardArgs a) {
   constexpr int kTeams = threads_of(TPR) / TPR;

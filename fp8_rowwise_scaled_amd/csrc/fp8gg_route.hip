@@ -23,11 +23,22 @@
 // them itself.
 //
 // 16384 tokens, 256 experts in 8 groups, k = 8, sigmoid and bias: 18 us for the choice (15
-// alone in a loop), 8.5 for the plan.  The logits (16.8 MB) take 3.2 us at a copy's rate;
-// what bounds the choice is its 1300 vector instructions per four tokens, and at its end
-// the few tokens decided in fp64 (up to 4 us after the others).  16 tokens, 8 experts: one
-// launch, 4.9 us.  64 tokens of the 256 experts: 9.9 us, 6.4 of them the choice, which is
-// one wave's chain of instructions from the load of a row to its weights.
+// alone in a loop), 8.5 for the plan.  The logits (16.8 MB) take 3.2 us at a copy's rate.
+// The choice's 1300 vector instructions per four tokens are 8.7 us of issue, 4 waves on each
+// SIMD; the rest is waiting: a workgroup of 64 tokens has 84 KB of LDS and a CU to itself, so
+// that all waves load, rank and finish in step, and the few tokens decided in fp64 end up to
+// 4 us after the others.
+//
+// What rows hold matters.  Rows with more candidates than the list has places go through
+// choose_in_rounds, and their wave waits.  16384 x 256, us, and with spread logits and k = 8:
+// k = 16, where 16 lanes give too low a bound, 104 and 19; one row in four of equal logits,
+// as padding leaves them, 73 and 19, in groups with a zero bias 170 and 27 (with a bias that
+// tells the experts apart 26); softmax with a bias, whose fp32 keys are told apart by 2^-16
+// alone, 30.
+//
+// 16 tokens, 8 experts: one launch, 4.9 us.  64 tokens of the 256 experts: 9.9 us, 6.4 of
+// them the choice, which is one wave's chain of instructions from the load of a row to its
+// weights.
 #include "fp8gg_layer_internal.h"
 
 namespace fp8gg {
