@@ -24,7 +24,7 @@
 //
 // 16384 tokens, 256 experts in 8 groups, k = 8, sigmoid and bias: 18 us for the choice (15
 // alone in a loop), 8.5 for the plan.  The logits (16.8 MB) take 3.2 us at a copy's rate.
-// The choice's 1300 vector instructions per four tokens are 8.7 us of issue, 4 waves on each
+// The choice's 1350 vector instructions per four tokens are 9 us of issue, 4 waves on each
 // SIMD; the rest is waiting: a workgroup of 64 tokens has 84 KB of LDS and a CU to itself, so
 // that all waves load, rank and finish in step, and the few tokens decided in fp64 end up to
 // 4 us after the others.
