@@ -57,3 +57,13 @@ from .layer import (  # noqa: F401
     f8f8bf16_silu_mul_backward,
     f8f8bf16_silu_mul_quantize,
 )
+from .train import (  # noqa: F401
+    WeightBlocks,
+    bf16_grouped_stacked,
+    bf16_grouped_stacked_dgrad,
+    bf16_grouped_stacked_wgrad,
+    f8f8bf16_grad_clip,
+    f8f8bf16_grad_square_sum,
+    f8f8bf16_quantize_groupwise,
+    f8f8bf16_quantize_groupwise_weight,
+)

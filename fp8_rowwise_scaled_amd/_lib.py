@@ -1,5 +1,5 @@
-"""ctypes loader for libfp8gg.so (the C ABI declared in include/fp8gg.h and
-include/fp8gg_layer.h)."""
+"""ctypes loader for libfp8gg.so (the C ABI declared in include/fp8gg.h,
+include/fp8gg_layer.h and include/fp8gg_train.h)."""
 from __future__ import annotations
 
 import ctypes
@@ -66,6 +66,19 @@ LAYER_EXPORTS = (
     "f8f8bf16_quantize_k_offsets_workspace",
     "f8f8bf16_k_offsets_capacity",
     "f8f8bf16_layer_last_error",
+)
+
+# Every symbol include/fp8gg_train.h declares.
+TRAIN_EXPORTS = (
+    "bf16_grouped_stacked",
+    "bf16_grouped_stacked_dgrad",
+    "bf16_grouped_stacked_wgrad",
+    "bf16_grouped_stacked_wgrad_workspace",
+    "f8f8bf16_quantize_groupwise",
+    "f8f8bf16_quantize_groupwise_weight",
+    "f8f8bf16_grad_square_sum",
+    "f8f8bf16_grad_clip",
+    "f8f8bf16_grad_workspace",
 )
 
 SCORE_SOFTMAX = 0
@@ -156,7 +169,17 @@ def load() -> ctypes.CDLL:
     lib.f8f8bf16_quantize_k_offsets.argtypes = [P, I, P, I64, P, P, P, P, P, I64, I64, I64, I64, P]
     lib.f8f8bf16_quantize_k_offsets_workspace.argtypes = [I64, I64, I64]
     lib.f8f8bf16_k_offsets_capacity.argtypes = [I64, I64]
-    for name in LAYER_EXPORTS:
+    D = ctypes.c_double
+    lib.bf16_grouped_stacked.argtypes = [P, P, P, P, I64, I64, I64, I64, P]
+    lib.bf16_grouped_stacked_dgrad.argtypes = [P, P, P, P, I64, I64, I64, I64, P]
+    lib.bf16_grouped_stacked_wgrad.argtypes = [P, P, P, P, I, I, P, I64, I64, I64, I64, I64, P]
+    lib.bf16_grouped_stacked_wgrad_workspace.argtypes = [I64, I64, I64, I64]
+    lib.f8f8bf16_quantize_groupwise.argtypes = [P, P, P, I64, I64, P]
+    lib.f8f8bf16_quantize_groupwise_weight.argtypes = [P, I, P, P, P, P, I64, I64, I64, P]
+    lib.f8f8bf16_grad_square_sum.argtypes = [P, P, P, I64, P, P, I64, P]
+    lib.f8f8bf16_grad_clip.argtypes = [P, P, P, P, I64, P, D, D, P, P, I64, P]
+    lib.f8f8bf16_grad_workspace.argtypes = [I64]
+    for name in LAYER_EXPORTS + TRAIN_EXPORTS:
         getattr(lib, name).restype = I64 if name.endswith(("_workspace", "_capacity")) else I
     lib.f8f8bf16_layer_last_error.restype = ctypes.c_char_p
     _lib = lib

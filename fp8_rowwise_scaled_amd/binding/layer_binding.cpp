@@ -1,11 +1,11 @@
-// CPython module fp8_rowwise_scaled_amd._layer_binding: torch tensors in, the C ABI of
-// fp8gg_layer.h, torch tensors out.
+// CPython module fp8_rowwise_scaled_amd._layer_binding: torch tensors in, the C ABIs of
+// fp8gg_layer.h and fp8gg_train.h, torch tensors out.
 //
 // A decode step's calls run 3 to 5 us on the GPU.  Checked and allocated from Python
 // they took 9 to 13 us of host time each (one allocation 1.3 to 1.6 us, a tensor's check
 // 0.3 us); here a norm with four outputs takes 6, the launch itself about 3.
 //
-// Arguments come in the fixed order that layer.py hands on.  Every tensor is checked
+// Arguments come in the fixed order that layer.py and train.py hand on.  Every tensor is checked
 // (type, shape, device, layout) before the library is called, which checks the rest;
 // outputs that are None are allocated on the inputs' device, and the work goes to that
 // device's current stream.  Errors become ValueError, or RuntimeError for a launch that
@@ -24,8 +24,10 @@
 #include <cstdarg>
 #include <cstdint>
 #include <string>
+#include <vector>
 
 #include "fp8gg_layer.h"
+#include "fp8gg_train.h"
 
 namespace {
 
@@ -58,6 +60,7 @@ const char* name_of(at::ScalarType t) {
     case at::kByte: return "torch.uint8";
     case at::kInt: return "torch.int32";
     case at::kLong: return "torch.int64";
+    case at::kDouble: return "torch.float64";
     default: return c10::toString(t);
   }
 }
@@ -157,6 +160,36 @@ class Call {
     return *given;
   }
 
+  // The next argument as a list or tuple of float32 or bf16 tensors of one device, each dense (in
+  // any order of its axes: every value is dealt with by itself).  None: nothing.
+  std::vector<const at::Tensor*> tensors(const char* what) {
+    PyObject* o = args_[at_++];
+    std::vector<const at::Tensor*> list;
+    if (o == Py_None) return list;
+    if (!PyList_Check(o) && !PyTuple_Check(o)) refuse("%s must be a list or tuple of tensors", what);
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+    list.reserve(n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      PyObject* e = PySequence_Fast_GET_ITEM(o, i);
+      if (!THPVariable_Check(e)) refuse("%s[%zd] must be a tensor", what, i);
+      const at::Tensor& x = THPVariable_Unpack(e);
+      if (x.layout() != at::kStrided) refuse("%s[%zd] must be a dense tensor", what, i);
+      if (x.scalar_type() != at::kFloat && x.scalar_type() != at::kBFloat16)
+        refuse("%s[%zd] must be bfloat16 or float32, got %s", what, i, name_of(x.scalar_type()));
+      if (!x.is_non_overlapping_and_dense()) refuse("%s[%zd] must be dense (a view with gaps or repeats is not)", what, i);
+      list.push_back(&x);
+    }
+    for (const at::Tensor* x : list) on_device(*x, what);
+    return list;
+  }
+  // For calls without any tensor: the current device.
+  void settle() {
+    if (placed_) return;
+    device_ = c10::Device(c10::DeviceType::CUDA, c10::hip::current_device());
+    guard_.reset_device(device_);
+    placed_ = true;
+  }
+
   // Makes the library's call on the tensors' device and its current stream, without the
   // interpreter's lock.  The library throws nothing, but a tensor that has no memory (one of
   // a tracer's) throws when it is asked for its address.
@@ -178,6 +211,10 @@ class Call {
   void place(const at::Tensor& t, const char* what) {
     if (!t.is_cuda()) refuse("%s must be on the GPU", what);
     if (!t.is_contiguous()) refuse("%s must be contiguous", what);
+    on_device(t, what);
+  }
+  void on_device(const at::Tensor& t, const char* what) {
+    if (!t.is_cuda()) refuse("%s must be on the GPU", what);
     if (!placed_) {
       device_ = t.device();
       guard_.reset_device(device_);
@@ -515,6 +552,184 @@ PyObject* quantize_k_offsets(PyObject* const* args, Py_ssize_t n) {
   return pack(XT, t_scale, k_offsets);
 }
 
+// X [total_M, K], W [G, N, K] and M_sizes [G] of a product by group.
+void check_weights(Call& c, const at::Tensor& W, const at::Tensor& M_sizes) {
+  c.check(W, "W", at::kBFloat16, 3, "[G, N, K]");
+  c.check(M_sizes, "M_sizes", at::kLong, {W.size(0)});
+}
+
+PyObject* grouped_product(PyObject* const* args, Py_ssize_t n) {
+  Call c("bf16_grouped_stacked", args, n, 4);
+  const at::Tensor& X = *c.tensor("X");
+  const at::Tensor& W = *c.tensor("W");
+  const at::Tensor& M_sizes = *c.tensor("M_sizes");
+  c.check(X, "X", at::kBFloat16, 2, "[total_M, K]");
+  check_weights(c, W, M_sizes);
+  const int64_t M = X.size(0), G = W.size(0), N = W.size(1), K = W.size(2);
+  c.check(X, "X", at::kBFloat16, {M, K});
+  const at::Tensor Y = c.output("Y", at::kBFloat16, {M, N});
+  c.run([&](void* stream) {
+    return bf16_grouped_stacked(ptr<uint16_t>(&X), ptr<uint16_t>(&W), ptr<int64_t>(&M_sizes), ptr<uint16_t>(Y), G, M, N, K,
+                                stream);
+  });
+  return wrap(Y);
+}
+
+PyObject* grouped_dgrad(PyObject* const* args, Py_ssize_t n) {
+  Call c("bf16_grouped_stacked_dgrad", args, n, 4);
+  const at::Tensor& dY = *c.tensor("dY");
+  const at::Tensor& W = *c.tensor("W");
+  const at::Tensor& M_sizes = *c.tensor("M_sizes");
+  c.check(dY, "dY", at::kBFloat16, 2, "[total_M, N]");
+  check_weights(c, W, M_sizes);
+  const int64_t M = dY.size(0), G = W.size(0), N = W.size(1), K = W.size(2);
+  c.check(dY, "dY", at::kBFloat16, {M, N});
+  const at::Tensor dX = c.output("dX", at::kBFloat16, {M, K});
+  c.run([&](void* stream) {
+    return bf16_grouped_stacked_dgrad(ptr<uint16_t>(&dY), ptr<uint16_t>(&W), ptr<int64_t>(&M_sizes), ptr<uint16_t>(dX), G, M,
+                                      N, K, stream);
+  });
+  return wrap(dX);
+}
+
+PyObject* grouped_wgrad(PyObject* const* args, Py_ssize_t n) {
+  Call c("bf16_grouped_stacked_wgrad", args, n, 7);
+  const at::Tensor& dY = *c.tensor("dY");
+  const at::Tensor& X = *c.tensor("X");
+  const at::Tensor& M_sizes = *c.tensor("M_sizes");
+  c.check(dY, "dY", at::kBFloat16, 2, "[total_M, N]");
+  c.check(X, "X", at::kBFloat16, 2, "[total_M, K]");
+  const int64_t M = dY.size(0), N = dY.size(1), K = X.size(1);
+  c.check(X, "X", at::kBFloat16, {M, K});
+  c.check(M_sizes, "M_sizes", at::kLong, 1, "[G]");
+  const int64_t G = M_sizes.size(0);
+  const bool f32 = c.flag();
+  const at::Tensor* given = c.tensor("dW", true);
+  const bool accumulate = c.flag();
+  if (accumulate && !given) refuse("accumulate needs a dW to add to");
+  at::Tensor dW;
+  if (given) {
+    c.check(*given, "dW", c.float_type(*given, "dW") == FP8GG_DTYPE_F32 ? at::kFloat : at::kBFloat16, {G, N, K});
+    dW = *given;
+  } else {
+    dW = c.fresh(f32 ? at::kFloat : at::kBFloat16, {G, N, K});
+  }
+  const at::Tensor ws = c.workspace(bf16_grouped_stacked_wgrad_workspace(G, M, N, K));
+  c.run([&](void* stream) {
+    return bf16_grouped_stacked_wgrad(ptr<uint16_t>(&dY), ptr<uint16_t>(&X), ptr<int64_t>(&M_sizes), dW.data_ptr(),
+                                      dW.scalar_type() == at::kFloat ? FP8GG_DTYPE_F32 : FP8GG_DTYPE_BF16, accumulate,
+                                      ptr<void>(ws), ws.defined() ? (int64_t)ws.nbytes() : 0, G, M, N, K, stream);
+  });
+  return wrap(dW);
+}
+
+PyObject* quantize_groupwise(PyObject* const* args, Py_ssize_t n) {
+  Call c("f8f8bf16_quantize_groupwise", args, n, 3);
+  const at::Tensor& X = *c.tensor("X");
+  c.check(X, "X", at::kBFloat16, 2, "[rows, K]");
+  const int64_t rows = X.size(0), K = X.size(1);
+  if (K % 128) refuse("X needs a multiple of 128 columns, got %lld", (long long)K);
+  const at::Tensor XQ = c.output("XQ", at::kByte, {rows, K});
+  const at::Tensor x_scale = c.output("x_scale", at::kFloat, {rows, K / 128});
+  c.run([&](void* stream) {
+    return f8f8bf16_quantize_groupwise(ptr<uint16_t>(&X), ptr<uint8_t>(XQ), ptr<float>(x_scale), rows, K, stream);
+  });
+  return pack(XQ, x_scale);
+}
+
+// A weight's output: [G, rows, cols], or [rows, cols] where the weight has no groups.
+at::Tensor weight_output(Call& c, const char* what, at::ScalarType type, bool groups, int64_t G, int64_t rows, int64_t cols) {
+  return groups ? c.output(what, type, {G, rows, cols}) : c.output(what, type, {rows, cols});
+}
+
+PyObject* quantize_weight(PyObject* const* args, Py_ssize_t n) {
+  Call c("f8f8bf16_quantize_groupwise_weight", args, n, 6);
+  const at::Tensor& W = *c.tensor("W");
+  const int dtype = c.float_type(W, "W");
+  const bool groups = W.dim() == 3;
+  if (!groups && W.dim() != 2) refuse("W must be [G, N, K] or [N, K]");
+  c.check(W, "W", W.scalar_type(), W.dim(), "[G, N, K] or [N, K]");
+  const int64_t G = groups ? W.size(0) : 1, N = W.size(W.dim() - 2), K = W.size(W.dim() - 1);
+  if (N % 128 || K % 128) refuse("W needs multiples of 128 rows and columns, got %lld and %lld", (long long)N, (long long)K);
+  const bool transposed = c.flag();
+  const at::Tensor WQ = weight_output(c, "WQ", at::kByte, groups, G, N, K);
+  const at::Tensor w_scale = weight_output(c, "w_scale", at::kFloat, groups, G, N / 128, K / 128);
+  at::Tensor WQt, wt_scale;
+  if (transposed || !c.none(0) || !c.none(1)) {
+    WQt = weight_output(c, "WQt", at::kByte, groups, G, K, N);
+    wt_scale = weight_output(c, "wt_scale", at::kFloat, groups, G, K / 128, N / 128);
+  }
+  c.run([&](void* stream) {
+    return f8f8bf16_quantize_groupwise_weight(W.data_ptr(), dtype, ptr<uint8_t>(WQ), ptr<float>(w_scale), ptr<uint8_t>(WQt),
+                                              ptr<float>(wt_scale), G, N, K, stream);
+  });
+  return pack(WQ, w_scale, WQt, wt_scale);
+}
+
+// Tensors of a call as the library takes them.
+struct Pointers {
+  std::vector<const void*> g;
+  std::vector<void*> out;
+  std::vector<int64_t> counts;
+  std::vector<int32_t> dtypes;
+  explicit Pointers(const std::vector<const at::Tensor*>& list) {
+    g.reserve(list.size());
+    counts.reserve(list.size());
+    dtypes.reserve(list.size());
+    for (const at::Tensor* t : list) {
+      g.push_back(t->numel() ? t->const_data_ptr() : nullptr);
+      counts.push_back(t->numel());
+      dtypes.push_back(t->scalar_type() == at::kFloat ? FP8GG_DTYPE_F32 : FP8GG_DTYPE_BF16);
+    }
+  }
+};
+
+PyObject* grad_square_sum(PyObject* const* args, Py_ssize_t n) {
+  Call c("f8f8bf16_grad_square_sum", args, n, 3);
+  if (c.none()) refuse("grads must be a list or tuple of tensors");
+  const auto list = c.tensors("grads");
+  c.settle();
+  const int64_t count = (int64_t)list.size();
+  const at::Tensor sum = c.output("square_sum", at::kDouble, {1});
+  const at::Tensor ws = c.workspace(f8f8bf16_grad_workspace(count));
+  const Pointers p(list);
+  c.run([&](void* stream) {
+    return f8f8bf16_grad_square_sum(p.g.data(), p.counts.data(), p.dtypes.data(), count, ptr<double>(sum), ptr<void>(ws),
+                                    ws.defined() ? (int64_t)ws.nbytes() : 0, stream);
+  });
+  return wrap(sum);
+}
+
+PyObject* grad_clip(PyObject* const* args, Py_ssize_t n) {
+  Call c("f8f8bf16_grad_clip", args, n, 7);
+  if (c.none()) refuse("grads must be a list or tuple of tensors");
+  const auto list = c.tensors("grads");
+  c.settle();
+  const int64_t count = (int64_t)list.size();
+  const double max_norm = c.number(), eps = c.number();
+  const at::Tensor* sum = c.tensor("square_sum", true);
+  if (sum) c.check(*sum, "square_sum", at::kDouble, {1});
+  const bool in_place = c.none();
+  const auto outs = c.tensors("outs");
+  if (!in_place && outs.size() != list.size()) refuse("outs has %zu tensors, grads %zu", outs.size(), list.size());
+  Pointers p(list);
+  p.out.reserve(list.size());
+  for (size_t i = 0; i < list.size(); ++i) {
+    const at::Tensor& o = in_place ? *list[i] : *outs[i];
+    if (o.scalar_type() != list[i]->scalar_type() || !o.sizes().equals(list[i]->sizes()) ||
+        !o.strides().equals(list[i]->strides()))
+      refuse("outs[%zu] must have the type, shape and strides of grads[%zu]", i, i);
+    p.out.push_back(o.numel() ? o.data_ptr() : nullptr);
+  }
+  const at::Tensor norm = c.output("norm", at::kFloat, {1});
+  const at::Tensor ws = c.workspace(sum ? 0 : f8f8bf16_grad_workspace(count));
+  c.run([&](void* stream) {
+    return f8f8bf16_grad_clip(p.g.data(), p.out.data(), p.counts.data(), p.dtypes.data(), count, ptr<double>(sum), max_norm, eps,
+                              ptr<float>(norm), ptr<void>(ws), ws.defined() ? (int64_t)ws.nbytes() : 0, stream);
+  });
+  return wrap(norm);
+}
+
 // No C++ exception leaves the module.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -544,6 +759,13 @@ PyMethodDef methods[] = {
     method<silu_mul_quantize>("silu_mul_quantize"),
     method<silu_mul_backward>("silu_mul_backward"),
     method<quantize_k_offsets>("quantize_k_offsets"),
+    method<grouped_product>("grouped_product"),
+    method<grouped_dgrad>("grouped_dgrad"),
+    method<grouped_wgrad>("grouped_wgrad"),
+    method<quantize_groupwise>("quantize_groupwise"),
+    method<quantize_weight>("quantize_weight"),
+    method<grad_square_sum>("grad_square_sum"),
+    method<grad_clip>("grad_clip"),
     {nullptr, nullptr, 0, nullptr},
 };
 

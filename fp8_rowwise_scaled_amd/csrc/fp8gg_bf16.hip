@@ -1,0 +1,626 @@
+// Products of bf16 matrices by group for gfx950: the forward product of the experts, the gradient
+// of its input and that of its weights.
+//
+//     Y[m, n]  = sum_k X[m, k] W[g, n, k]        both operands run along the contraction
+//     dX[m, k] = sum_n dY[m, n] W[g, n, k]       W runs across it
+//     dW[g, n, k] = sum_m dY[m, n] X[m, k]       both run across it, over the rows of a group
+//
+// One tile serves all three: an operand that runs along the contraction is read from LDS sixteen
+// bytes a lane, one that runs across it with the transposing read (ds_read_b64_tr_b16), so no
+// transposed copy of anything is made.  v_mfma_f32_32x32x16_bf16 with the output's columns as its rows,
+// fp32 accumulators; tiles go global -> LDS without registers.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp8gg_lds.h"
+#include "fp8gg_layer_internal.h"
+#include "fp8gg_train_internal.h"
+
+namespace fp8gg {
+
+namespace {
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) v4s* lds_v4s;
+
+// ---------------------------------------------------------------------------
+// Groups: rows of each, from the counts on the device
+// ---------------------------------------------------------------------------
+
+struct SatAdd {
+  uint32_t cap;
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return umin(a + b, cap); }
+};
+struct AddU {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a + b; }
+};
+
+__device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+}
+
+// Rows [start, end) of the 64 groups from g0 on, one per lane; `rows`: the rows before them.
+__device__ __forceinline__ void group_rows(const ProductArgs& a, int g0, uint32_t rows, uint32_t& start, uint32_t& end) {
+  const int lane = threadIdx.x & 63;
+  const int64_t n = g0 + lane < a.G ? a.M_sizes[g0 + lane] : 0;
+  const uint32_t M = (uint32_t)a.M;
+  const uint32_t c = n <= 0 ? 0u : n >= a.M ? M : (uint32_t)n;
+  end = umin(wave_scan(c, SatAdd{M}) + rows, M);
+  const uint32_t before = (uint32_t)__shfl_up((int)end, 1, 64);
+  start = lane ? before : rows;
+}
+
+struct RowTile {
+  int g;
+  int64_t row0, row_end;
+};
+
+// Tiles of BM rows over all groups: first those with more than BM / 2 rows, then the others (at
+// most one per group), so that a persistent grid meets its cheap tiles last.
+struct RowTiles {
+  uint32_t tall, all;
+};
+
+template <int BM>
+__device__ __forceinline__ RowTiles count_row_tiles(const ProductArgs& a) {
+  uint32_t rows = 0;
+  RowTiles n = {0, 0};
+  for (int g0 = 0; g0 < a.G; g0 += 64) {
+    uint32_t start, end;
+    group_rows(a, g0, rows, start, end);
+    n.tall += lane_value(wave_scan((end - start + BM / 2 - 1) / BM, AddU{}), 63);
+    n.all += lane_value(wave_scan((end - start + BM - 1) / BM, AddU{}), 63);
+    rows = lane_value(end, 63);
+  }
+  return n;
+}
+
+template <int BM>
+__device__ __forceinline__ RowTile find_row_tile(const ProductArgs& a, const RowTiles& n, uint32_t tile) {
+  const bool tall = tile < n.tall;
+  tile -= tall ? 0 : n.tall;
+  uint32_t rows = 0, tiles = 0;
+  for (int g0 = 0; g0 < a.G; g0 += 64) {
+    uint32_t start, end;
+    group_rows(a, g0, rows, start, end);
+    const uint32_t high = (end - start + BM / 2 - 1) / BM;
+    const uint32_t mine = tall ? high : (end - start + BM - 1) / BM - high;
+    const uint32_t upto = tiles + wave_scan(mine, AddU{});
+    const uint64_t hit = __ballot(tile < upto);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      const uint32_t nth = tile - lane_value(upto - mine, l) + (tall ? 0 : lane_value(high, l));
+      return {g0 + l, lane_value(start, l) + (int64_t)nth * BM, (int64_t)lane_value(end, l)};
+    }
+    tiles = lane_value(upto, 63);
+    rows = lane_value(end, 63);
+  }
+  return {0, 0, 0};
+}
+
+// Rows of one group, and (up to 64 groups) the group that comes nth when they are taken by size,
+// the largest first.
+__device__ __forceinline__ void nth_group(const ProductArgs& a, int& g, int64_t& first, int64_t& count) {
+  uint32_t rows = 0, start, end;
+  if (a.G <= 64) {
+    group_rows(a, 0, 0, start, end);
+    const int lane = threadIdx.x & 63;
+    const uint32_t mine = end - start;
+    int rank = 0;
+    for (int o = 0; o < (int)a.G; ++o) {
+      const uint32_t other = lane_value(mine, o);
+      rank += other > mine || (other == mine && o < lane);
+    }
+    g = __builtin_ctzll(__ballot(lane < a.G && rank == g));
+  } else {
+    for (int g0 = 0;; g0 += 64) {
+      group_rows(a, g0, rows, start, end);
+      if (g < g0 + 64) break;
+      rows = lane_value(end, 63);
+    }
+  }
+  first = lane_value(start, g & 63);
+  count = lane_value(end, g & 63) - first;
+}
+
+// ---------------------------------------------------------------------------
+// One output tile
+// ---------------------------------------------------------------------------
+
+// An operand of the tile in LDS: R rows (or columns) of the output by BK of the contraction.
+// ALONG: the contraction runs along memory; LDS rows are BK values, read 16 bytes a lane.
+// Else it runs across memory; LDS rows are the R values of one place in the contraction, and the
+// matrix instruction's operand is read transposed (ds_read_b64_tr_b16: sixteen lanes read four
+// places of sixteen values, lane i gets value i of the four).
+// PERM: the 32 columns of a block go to the instruction's rows in the order that leaves each lane
+// sixteen neighbouring columns of the result.
+template <int R, int BK, int NT, bool ALONG, bool PERM>
+struct Operand {
+  static constexpr int CHUNKS = R * BK / 8;
+  static constexpr int LOADS = CHUNKS / NT;
+  static constexpr int BYTES = R * BK * 2;
+  static constexpr int CPR = (ALONG ? BK : R) / 8;
+  static_assert(CHUNKS % NT == 0, "every thread copies as much");
+  const uint16_t* src[LOADS];
+  int at[LOADS];                 // the chunk's place in the contraction
+
+  // 16-byte chunk c of LDS row `row` lies at c ^ swz(row): no bank conflicts in either kind of read
+  // (across: the four places that sixteen lanes read lie in four different 64-byte columns).
+  static __device__ __forceinline__ int swz(int row) {
+    if constexpr (ALONG) return lds_swz<BK * 2>(row);
+    else if constexpr (R >= 128) return (row & 3) << 2;
+    else if constexpr (R == 64) return ((row >> 1) & 1) << 2;
+    else return 0;
+  }
+
+  // Chunks of the operand whose contraction starts at `base`: rows (columns) [first, first + count)
+  // of the matrix exist; the tile's other ones repeat the last and their results are dropped.
+  __device__ __forceinline__ void setup(const uint16_t* base, int64_t ld, int64_t first, int64_t count) {
+    const int tid = threadIdx.x % NT;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int q = i * NT + tid;
+      const int row = q / CPR;
+      const int c = (q % CPR) ^ swz(row);
+      if constexpr (ALONG) {
+        const int local = PERM ? (row & ~31) + 16 * ((row >> 2) & 1) + 4 * ((row & 31) >> 3) + (row & 3) : row;
+        const int64_t r = local < count ? local : count - 1;
+        src[i] = base + (first + r) * ld + c * 8;
+        at[i] = c * 8;
+      } else {
+        int64_t col = c * 8;
+        col = col < count ? col : count - 8;
+        src[i] = base + (int64_t)row * ld + first + col;
+        at[i] = row;
+      }
+    }
+  }
+
+  // Copy i of contraction [k, k + BK) of n; zeros from n on (for both operands, so that nothing
+  // that lies there, a NaN included, reaches a sum).
+  __device__ __forceinline__ void issue(int i, uint8_t* lds, int64_t k, int64_t n, int64_t ld) const {
+    const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x % NT) >> 6);
+    const void* p = src[i] + (ALONG ? k : k * ld);
+    if (k + BK > n && k + at[i] >= n) p = g_zero16;
+    copy16_to_lds(p, lds_addr(lds + (i * NT + wave * 64) * 16));
+  }
+
+  // The instruction's operand: block b of 32, step ks of 16 along the contraction.
+  static __device__ __forceinline__ v8bf frag(const uint8_t* lds, int b, int ks) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (ALONG) {
+      const int row = 32 * b + (lane & 31);
+      return *(const v8bf*)(lds + row * (BK * 2) + (((2 * ks + (lane >> 5)) ^ swz(row)) * 16));
+    } else {
+      const int i = lane & 15, half = (lane >> 4) & 1, h = lane >> 5;
+      const int four = 4 * half + (i & 3);               // which four of the block's 32
+      const int piece = 8 * b + (PERM ? 4 * (four & 1) + (four >> 1) : four);
+      const int k = 16 * ks + 8 * h + (i >> 2);
+      const uint8_t* p = lds + k * (R * 2) + ((piece >> 1) ^ swz(k)) * 16 + (piece & 1) * 8;
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p));
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p + 4 * R * 2));
+      return __builtin_bit_cast(v8bf, (v8s)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+// A BM x BN tile of the output by WM x WN waves.  P: the operand of the output's rows, in a ring of
+// SP slots of LDS; Q: of its columns, in SQ slots.
+template <bool P_ALONG, bool Q_ALONG, int BM, int BN, int BK, int WM, int WN, int SP, int SQ>
+struct ProductTile {
+  static constexpr int NT = WM * WN * 64;
+  static constexpr int FM = BM / WM / 32, FN = BN / WN / 32, KS = BK / 16;
+  typedef Operand<BM, BK, NT, P_ALONG, false> P;
+  typedef Operand<BN, BK, NT, Q_ALONG, true> Q;
+  static constexpr int SMEM = SP * P::BYTES + SQ * Q::BYTES;
+  static_assert(SP >= 2 && (SQ == SP || (SP == 2 && SQ == 3)), "the wait counts below");
+  static_assert(KS % 2 == 0, "operands alternate between two sets of registers");
+  typedef v16f Acc[FM][FN];
+
+  uint8_t* smem;
+  P p;
+  Q q;
+
+  __device__ __forceinline__ uint8_t* pslot(int i) const { return smem + i * P::BYTES; }
+  __device__ __forceinline__ uint8_t* qslot(int i) const { return smem + SP * P::BYTES + i * Q::BYTES; }
+  static __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((threadIdx.x % NT) >> 6); }
+  // A single wave orders its own copies and reads by its waits.
+  static __device__ __forceinline__ void barrier() {
+    if constexpr (NT > 64) block_barrier();
+    else asm volatile("" ::: "memory");
+  }
+
+  // acc += the products over a contraction of n.
+  __device__ __forceinline__ void run(int64_t n, int64_t ldp, int64_t ldq, Acc& acc) const {
+    const int wm = wave_id() / WN, wn = wave_id() % WN;
+    const int nk = (int)((n + BK - 1) / BK);
+    barrier();                                   // the last tile's reads of the ring are done
+    if (nk == 0) return;
+#pragma unroll
+    for (int s = 0; s < (SP > SQ - 1 ? SP : SQ - 1); ++s) {
+#pragma unroll
+      for (int i = 0; s < SP && i < P::LOADS; ++i) p.issue(i, pslot(s), (int64_t)s * BK, n, ldp);
+#pragma unroll
+      for (int i = 0; s < SQ - 1 && i < Q::LOADS; ++i) q.issue(i, qslot(s), (int64_t)s * BK, n, ldq);
+    }
+    wait_vmcnt_le((SP - 1) * P::LOADS + (SQ - 2) * Q::LOADS);
+    barrier();
+    v8bf pf[2][FM], qf[2][FN];
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) pf[0][fm] = P::frag(pslot(0), wm * FM + fm, 0);
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn) qf[0][fn] = Q::frag(qslot(0), wn * FN + fn, 0);
+    constexpr int NM = FM * FN, NR = FM + FN;    // instructions and operands of a step
+    constexpr int QS = KS - 1 < 2 ? KS - 1 : 2;  // steps over which Q's copies are spread
+    int sp = 0, sq = 0;
+    for (int kt = 0; kt < nk; ++kt) {
+      const int np = sp == SP - 1 ? 0 : sp + 1, nq = sq == SQ - 1 ? 0 : sq + 1, bq = sq == 0 ? SQ - 1 : sq - 1;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int c = ks & 1, d = c ^ 1;
+        const bool last = ks == KS - 1;
+        if (last) {
+          // this wave has read its last operands of stage kt, and stage kt + 1 has landed once only
+          // the younger copies are outstanding; the barrier says so of all waves
+          __builtin_amdgcn_s_waitcnt(0xC07F);    // lgkmcnt 0
+          wait_vmcnt_le(SP == SQ ? (SP - 2) * (P::LOADS + Q::LOADS) : Q::LOADS);
+          barrier();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+          const int fm = i / FN, fn = i % FN;
+          acc[fm][fn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[c][fn], pf[c][fm], acc[fm][fn], 0, 0, 0);
+          // the next step's operands (of the next stage in the last step; past the end they are read
+          // from the ring all the same and not used)
+#pragma unroll
+          for (int r = i * NR / NM; r < (i + 1) * NR / NM; ++r) {
+            const int rk = last ? 0 : ks + 1;
+            if (r < FN) qf[d][r] = Q::frag(qslot(last ? nq : sq), wn * FN + r, rk);
+            else pf[d][r - FN] = P::frag(pslot(last ? np : sp), wm * FM + r - FN, rk);
+          }
+          // P's copies into the slot that the last step has freed, Q's in the first steps after it
+          if (last) {
+#pragma unroll
+            for (int r = i * P::LOADS / NM; r < (i + 1) * P::LOADS / NM; ++r)
+              p.issue(r, pslot(sp), (int64_t)(kt + SP) * BK, n, ldp);
+          } else if (ks < QS) {
+#pragma unroll
+            for (int r = (ks * NM + i) * Q::LOADS / (QS * NM); r < (ks * NM + i + 1) * Q::LOADS / (QS * NM); ++r)
+              q.issue(r, qslot(bq), (int64_t)(kt + SQ - 1) * BK, n, ldq);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      sp = np;
+      sq = nq;
+    }
+    wait_vmcnt_le(0);                            // no copy is in flight when the ring is used again
+  }
+
+  // Rows [row0, row_end) and columns [col0, cols) of the output through the idle ring, so that every
+  // store covers whole rows of the tile, as many rows at a time as the ring holds.  F32: the output's
+  // type; else bf16, rounded to nearest even from the fp32 sum.
+  template <bool F32>
+  __device__ __forceinline__ void store(void* out, int64_t ldo, int64_t row0, int64_t row_end, int64_t col0, int64_t cols,
+                                        bool accumulate, const Acc& acc) const {
+    constexpr int PER = F32 ? 4 : 8;             // values of a 16-byte chunk
+    constexpr int CPR = BN / PER, MASK = (CPR < 16 ? CPR : 16) - 1;
+    constexpr int TILE = BM * BN * (F32 ? 4 : 2);
+    constexpr int PASSES = TILE <= SMEM ? 1 : TILE <= 2 * SMEM ? 2 : 4;
+    constexpr int ROWS = BM / PASSES, FP = FM / PASSES;
+    static_assert(ROWS * CPR * 16 <= SMEM && FM % PASSES == 0, "a pass fits the ring");
+    const int tid = threadIdx.x % NT, lane = tid & 63, h = lane >> 5, r32 = lane & 31;
+    const int wm = wave_id() / WN, wn = wave_id() % WN;
+#pragma unroll
+    for (int ps = 0; ps < PASSES; ++ps) {
+      barrier();
+#pragma unroll
+      for (int f = 0; f < FP; ++f) {
+        const int r = (wm * FP + f) * 32 + r32;
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn) {
+          const v16f& x = acc[ps * FP + f][fn];
+#pragma unroll
+          for (int e = 0; e < 16 / PER; ++e) {
+            const int chunk = (wn * FN + fn) * (32 / PER) + h * (16 / PER) + e;
+            v4i v;
+            if constexpr (F32)
+              v = __builtin_bit_cast(v4i, v4f{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]});
+            else
+              v = v4i{(int)pack_bf16x2(x[8 * e], x[8 * e + 1]), (int)pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
+                      (int)pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), (int)pack_bf16x2(x[8 * e + 6], x[8 * e + 7])};
+            *(v4i*)(smem + (r * CPR + (chunk ^ (r & MASK))) * 16) = v;
+          }
+        }
+      }
+      barrier();
+#pragma unroll 4
+      for (int i = tid; i < ROWS * CPR; i += NT) {
+        const int r = i / CPR, c = i % CPR;
+        const int64_t row = row0 + r / (32 * FP) * (32 * FM) + ps * FP * 32 + r % (32 * FP), col = col0 + PER * c;
+        if (row >= row_end || col >= cols) continue;
+        v4i v = *(const v4i*)(smem + (r * CPR + (c ^ (r & MASK))) * 16);
+        v4i* o = (v4i*)((uint8_t*)out + (row * ldo + col) * (F32 ? 4 : 2));
+        if constexpr (F32)
+          if (accumulate) v = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, v) + __builtin_bit_cast(v4f, *o));
+        store_out(o, v);
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Forward and the input's gradient: the output's rows are grouped
+// ---------------------------------------------------------------------------
+
+template <typename E, bool Q_ALONG>
+__device__ __forceinline__ void product_tile(const ProductArgs& a, uint8_t* smem, const RowTile& t, int64_t col0) {
+  E e;
+  e.smem = smem;
+  e.p.setup(a.P, a.L, t.row0, t.row_end - t.row0);
+  const int64_t ldq = Q_ALONG ? a.L : a.C;
+  e.q.setup(a.Q + t.g * a.L * a.C, ldq, col0, a.C - col0);
+  typename E::Acc acc = {};
+  e.run(a.L, a.L, ldq, acc);
+  e.template store<false>(a.out, a.C, t.row0, t.row_end, col0, a.C, false, acc);
+}
+
+// One tile per workgroup; workgroups past the last tile end at once.
+template <bool Q_ALONG, int BM, int BN, int BK, int WM, int WN, int SP, int SQ>
+__global__ void __launch_bounds__(WM * WN * 64, 2) product_kernel(ProductArgs a) {
+  typedef ProductTile<true, Q_ALONG, BM, BN, BK, WM, WN, SP, SQ> E;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[E::SMEM];
+  const RowTiles n = count_row_tiles<BM>(a);
+  const int64_t T = (int64_t)n.all * a.col_tiles;
+  if ((int64_t)blockIdx.x >= T) return;
+  const int64_t slot = xcd_slot(blockIdx.x, T);
+  product_tile<E, Q_ALONG>(a, smem, find_row_tile<BM>(a, n, (uint32_t)(slot / a.col_tiles)), slot % a.col_tiles * BN);
+}
+
+// One workgroup per compute unit; the tiles that do not fill a whole round of them are computed
+// as quarters where two rounds of these take less than a whole tile.
+template <bool Q_ALONG>
+__global__ void __launch_bounds__(512, 2) product_persistent_kernel(ProductArgs a) {
+  constexpr int BM = 256, BN = 256;
+  typedef ProductTile<true, Q_ALONG, BM, BN, 64, 2, 4, 2, 3> E;
+  typedef ProductTile<true, Q_ALONG, BM / 2, BN / 2, 64, 2, 4, 5, 5> H;
+  static_assert(H::SMEM <= E::SMEM, "quarters share the ring");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[E::SMEM];
+  const int64_t P = gridDim.x, w = xcd_slot(blockIdx.x, P);
+  const RowTiles n = count_row_tiles<BM>(a);
+  const int64_t T = (int64_t)n.all * a.col_tiles, tall = (int64_t)n.tall * a.col_tiles;
+  // of the last tiles, those with more than half the rows have four quarters, the others two
+  int64_t whole = T / P * P;
+  const int64_t four = tall > whole ? tall - whole : 0, two = T - whole - four;
+  const int64_t quarters = 4 * four + 2 * two;
+  if (quarters > 2 * P) whole = T;
+  for (int64_t tile = w; tile < whole; tile += P)
+    product_tile<E, Q_ALONG>(a, smem, find_row_tile<BM>(a, n, (uint32_t)(tile / a.col_tiles)), tile % a.col_tiles * BN);
+  if (whole == T) return;
+  for (int64_t i = w; i < quarters; i += P) {
+    const int64_t tile = whole + (i < 4 * four ? i / 4 : four + (i - 4 * four) / 2);
+    const int part = (int)(i < 4 * four ? i % 4 : (i - 4 * four) % 2);
+    RowTile t = find_row_tile<BM>(a, n, (uint32_t)(tile / a.col_tiles));
+    t.row0 += part / 2 * (BM / 2);
+    const int64_t col0 = tile % a.col_tiles * BN + part % 2 * (BN / 2);
+    if (t.row0 < t.row_end && col0 < a.C) product_tile<H, Q_ALONG>(a, smem, t, col0);
+  }
+}
+
+// Few tiles: the W waves of a workgroup take a part of the contraction each, in rings of their own,
+// and their sums are added in the order of the waves.
+template <bool Q_ALONG, int BN, int BK, int W, int SLOTS>
+__global__ void __launch_bounds__(W * 64) product_split_kernel(ProductArgs a) {
+  constexpr int BM = 32, FN = BN / 32;
+  typedef ProductTile<true, Q_ALONG, BM, BN, BK, 1, 1, SLOTS, SLOTS> E;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[W * E::SMEM];
+  static_assert(BM * BN * 4 <= E::SMEM, "a wave's sums fit its ring");
+  const RowTiles n = count_row_tiles<BM>(a);
+  const int64_t T = (int64_t)n.all * a.col_tiles;
+  if ((int64_t)blockIdx.x >= T) return;
+  const int64_t slot = xcd_slot(blockIdx.x, T);
+  const RowTile t = find_row_tile<BM>(a, n, (uint32_t)(slot / a.col_tiles));
+  const int64_t col0 = slot % a.col_tiles * BN;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t per = ((a.L + W - 1) / W + BK - 1) / BK * BK;
+  const int64_t k0 = wave * per, k1 = k0 + per < a.L ? k0 + per : a.L;
+  E e;
+  e.smem = smem + wave * E::SMEM;
+  const int64_t ldq = Q_ALONG ? a.L : a.C;
+  typename E::Acc acc = {};
+  if (k0 < k1) {
+    e.p.setup(a.P + k0, a.L, t.row0, t.row_end - t.row0);
+    e.q.setup(a.Q + t.g * a.L * a.C + (Q_ALONG ? k0 : k0 * a.C), ldq, col0, a.C - col0);
+    e.run(k1 - k0, a.L, ldq, acc);
+  }
+  // lane (h, r) holds row r, columns 32 fn + 16 h + i
+#pragma unroll
+  for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *((v4f*)e.smem + (fn * 4 + i) * 64 + lane) =
+          v4f{acc[0][fn][4 * i], acc[0][fn][4 * i + 1], acc[0][fn][4 * i + 2], acc[0][fn][4 * i + 3]};
+  __syncthreads();
+  // a thread: eight neighbouring columns of one row
+  for (int i = threadIdx.x; i < BM * BN / 8; i += W * 64) {
+    const int r = i / (BN / 8), c = i % (BN / 8);
+    const int64_t row = t.row0 + r, col = col0 + 8 * c;
+    if (row >= t.row_end || col >= a.C) continue;
+    const int from = (c / 4 * 4 + c % 2 * 2) * 64 + c / 2 % 2 * 32 + r;   // fn = c / 4, h = c / 2 % 2, i = 2 (c % 2)
+    v4f lo = {0.f, 0.f, 0.f, 0.f}, hi = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const v4f* s = (const v4f*)(smem + w * E::SMEM) + from;
+      lo += s[0];
+      hi += s[64];
+    }
+    store_out((v4i*)((uint16_t*)a.out + row * a.C + col),
+              v4i{(int)pack_bf16x2(lo.x, lo.y), (int)pack_bf16x2(lo.z, lo.w), (int)pack_bf16x2(hi.x, hi.y),
+                  (int)pack_bf16x2(hi.z, hi.w)});
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The weights' gradient: the contraction runs over a group's rows
+// ---------------------------------------------------------------------------
+
+// a.splits > 1: the group's rows in so many parts, each part's sums to a.partial.
+template <bool F32, int BM, int BN, int BK, int WM, int WN, int SP, int SQ>
+__global__ void __launch_bounds__(WM * WN * 64, 2) wgrad_kernel(ProductArgs a) {
+  typedef ProductTile<false, false, BM, BN, BK, WM, WN, SP, SQ> E;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[E::SMEM];
+  // every XCD takes an eighth of each group's tiles: groups differ in size
+  const int64_t per = a.row_tiles * a.col_tiles * a.splits, share = (per + 7) / 8;
+  const int64_t i = blockIdx.x / 8;
+  int64_t tile = blockIdx.x % 8 * share + i % share;
+  if (tile >= per) return;
+  int g = (int)(i / share);
+  int64_t first, count;
+  nth_group(a, g, first, count);
+  const int64_t part = tile % a.splits;
+  tile /= a.splits;
+  const int64_t row0 = tile / a.col_tiles * BM, col0 = tile % a.col_tiles * BN;
+  void* out = (uint8_t*)a.out + (int64_t)g * a.L * a.C * (F32 ? 4 : 2);
+  if (a.splits > 1) {
+    const int64_t rows = ((count + a.splits - 1) / a.splits + BK - 1) / BK * BK;
+    const int64_t from = part * rows < count ? part * rows : count;
+    first += from;
+    count = rows < count - from ? rows : count - from;
+    out = (float*)a.partial + (part * a.G + g) * a.L * a.C;
+  }
+  E e;
+  e.smem = smem;
+  e.p.setup(a.P + first * a.L, a.L, row0, a.L - row0);
+  e.q.setup(a.Q + first * a.C, a.C, col0, a.C - col0);
+  if (F32 && a.splits == 1 && a.accumulate && count == 0) return;
+  typename E::Acc acc = {};
+  e.run(count, a.L, a.C, acc);
+  e.template store<F32>(out, a.C, row0, a.L, col0, a.C, F32 && a.splits == 1 && a.accumulate, acc);
+}
+
+// The parts' sums added in their order.
+template <bool F32>
+__global__ void __launch_bounds__(256) wgrad_join_kernel(ProductArgs a) {
+  const int64_t n = a.G * a.L * a.C / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    v4f lo = {0.f, 0.f, 0.f, 0.f}, hi = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t s = 0; s < a.splits; ++s) {
+      const v4f* p = (const v4f*)a.partial + (s * n + i) * 2;
+      lo += p[0];
+      hi += p[1];
+    }
+    if constexpr (F32) {
+      v4f* o = (v4f*)a.out + 2 * i;
+      if (a.accumulate) {
+        lo += o[0];
+        hi += o[1];
+      }
+      o[0] = lo;
+      o[1] = hi;
+    } else {
+      store_out((v4i*)a.out + i, v4i{(int)pack_bf16x2(lo.x, lo.y), (int)pack_bf16x2(lo.z, lo.w), (int)pack_bf16x2(hi.x, hi.y),
+                                     (int)pack_bf16x2(hi.z, hi.w)});
+    }
+  }
+}
+
+}  // namespace
+
+namespace {
+
+constexpr int64_t kWgradRows = 256, kWgradCols = 128;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Row tiles of the grouped output, whatever the groups' sizes.
+int64_t most_row_tiles(const ProductArgs& a, int64_t BM) { return a.M / BM + (a.G < a.M ? a.G : a.M); }
+
+enum Variant { kSplit, kRows32, kRows128, kPersistent };
+
+Variant variant_of(const ProductArgs& a) {
+  if (most_row_tiles(a, 32) * cdiv(a.C, 128) <= 256) return kSplit;
+  const int64_t rows = a.M / a.G;
+  if (rows < 24) return kRows32;
+  if (rows < 192) return kRows128;
+  return kPersistent;
+}
+
+template <bool Q_ALONG>
+hipError_t launch_rows(ProductArgs a, int cus, hipStream_t stream) {
+  switch (variant_of(a)) {
+    case kSplit: {
+      constexpr int BN = Q_ALONG ? 32 : 64;
+      a.col_tiles = cdiv(a.C, BN);
+      const dim3 grid((uint32_t)(most_row_tiles(a, 32) * a.col_tiles));
+      if constexpr (Q_ALONG) hipLaunchKernelGGL((product_split_kernel<true, 32, 64, 4, 4>), grid, dim3(256), 0, stream, a);
+      else hipLaunchKernelGGL((product_split_kernel<false, 64, 32, 8, 3>), grid, dim3(512), 0, stream, a);
+      break;
+    }
+    case kRows32:
+      a.col_tiles = cdiv(a.C, 128);
+      hipLaunchKernelGGL((product_kernel<Q_ALONG, 32, 128, 64, 1, 4, 4, 4>), dim3((uint32_t)(most_row_tiles(a, 32) * a.col_tiles)),
+                         dim3(256), 0, stream, a);
+      break;
+    case kRows128:
+      a.col_tiles = cdiv(a.C, 128);
+      hipLaunchKernelGGL((product_kernel<Q_ALONG, 128, 128, 64, 2, 2, 2, 3>),
+                         dim3((uint32_t)(most_row_tiles(a, 128) * a.col_tiles)), dim3(256), 0, stream, a);
+      break;
+    case kPersistent:
+      a.col_tiles = cdiv(a.C, 256);
+      hipLaunchKernelGGL((product_persistent_kernel<Q_ALONG>), dim3((uint32_t)cus), dim3(512), 0, stream, a);
+      break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t product_grid(const ProductArgs& a) {
+  switch (variant_of(a)) {
+    case kRows32: return most_row_tiles(a, 32) * cdiv(a.C, 128);
+    case kRows128: return most_row_tiles(a, 128) * cdiv(a.C, 128);
+    default: return most_row_tiles(a, 256) * cdiv(a.C, 256);    // tiles, which are counted in 32 bits
+  }
+}
+
+hipError_t launch_product(bool transposed, ProductArgs a, int cus, hipStream_t stream) {
+  return transposed ? launch_rows<false>(a, cus, stream) : launch_rows<true>(a, cus, stream);
+}
+
+int wgrad_splits(int64_t G, int64_t M, int64_t N, int64_t K) {
+  if (G <= 0 || M <= 0 || N <= 0 || K <= 0) return 1;
+  const int64_t tiles = G * cdiv(N, kWgradRows) * cdiv(K, kWgradCols);
+  int64_t s = cdiv(512, tiles);
+  const int64_t most = M / G / 256;
+  s = s < most ? s : most;
+  s = s < 32 ? s : 32;
+  return tiles >= 256 || s < 1 ? 1 : (int)s;
+}
+
+int64_t wgrad_grid(const ProductArgs& a) {
+  return a.G * cdiv(cdiv(a.L, kWgradRows) * cdiv(a.C, kWgradCols) * wgrad_splits(a.G, a.M, a.L, a.C), 8) * 8;
+}
+
+hipError_t launch_wgrad(bool f32, ProductArgs a, hipStream_t stream) {
+  a.row_tiles = cdiv(a.L, kWgradRows);
+  a.col_tiles = cdiv(a.C, kWgradCols);
+  a.splits = wgrad_splits(a.G, a.M, a.L, a.C);
+  const dim3 grid((uint32_t)wgrad_grid(a));
+  if (f32 || a.splits > 1) hipLaunchKernelGGL((wgrad_kernel<true, 256, 128, 32, 2, 2, 3, 3>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((wgrad_kernel<false, 256, 128, 32, 2, 2, 3, 3>), grid, dim3(256), 0, stream, a);
+  if (a.splits > 1) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t blocks = cdiv(a.G * a.L * a.C / 8, 256);
+    const dim3 join((uint32_t)(blocks < 2048 ? blocks : 2048));
+    if (f32) hipLaunchKernelGGL((wgrad_join_kernel<true>), join, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((wgrad_join_kernel<false>), join, dim3(256), 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace fp8gg
