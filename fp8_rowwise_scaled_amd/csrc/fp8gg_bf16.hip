@@ -7,10 +7,18 @@
 //
 // One tile serves all three: an operand that runs along the contraction is read from LDS sixteen
 // bytes a lane, one that runs across it with the transposing read (ds_read_b64_tr_b16), so no
-// transposed copy of anything is made.  v_mfma_f32_32x32x16_bf16 with the output's columns as its rows,
+// transposed copy of anything is made.  v_mfma_f32_16x16x32_bf16 with the output's columns as its rows,
 // fp32 accumulators; tiles go global -> LDS without registers.
+//
+// What bounds it: on data as it comes the card's power.  A product of 4096 x 4096 x 7168 takes 126 us
+// on zeros and 161 on normal values (2.4 GHz against about 1.9), so what moves fewer bits counts as
+// much as what waits less: 16 x 16 x 32 instead of 32 x 32 x 16 instructions, which write half the sums per
+// product, 198 -> 176 us; copies addressed by a scalar base and a fixed offset per lane (no vector
+// arithmetic in the loop), 169 -> 164; neighbouring instructions that share an operand, 164 -> 163.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "fp8gg_lds.h"
 #include "fp8gg_layer_internal.h"
@@ -20,6 +28,7 @@ namespace fp8gg {
 
 namespace {
 
+typedef int v2i __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -58,7 +67,7 @@ struct RowTile {
 };
 
 // Tiles of BM rows over all groups: first those with more than BM / 2 rows, then the others (at
-// most one per group), so that a persistent grid meets its cheap tiles last.
+// most one per group).
 struct RowTiles {
   uint32_t tall, all;
 };
@@ -125,26 +134,60 @@ __device__ __forceinline__ void nth_group(const ProductArgs& a, int& g, int64_t&
   count = lane_value(end, g & 63) - first;
 }
 
+// xcd_slot in 32 bits (the launcher's bound on the tiles).
+__device__ __forceinline__ uint32_t xcd_slot32(uint32_t w, uint32_t P) {
+  const uint32_t x = w % 8, q = P / 8, r = P % 8;
+  return x * q + (x < r ? x : r) + w / 8;
+}
+
+// Tiles of a rows x cols grid in strips of four rows, column by column: the 32 tiles that an XCD works on
+// at a time are four rows by eight columns (12 panels of the operands to read), not one row or two
+// (18 to 30).  Input's gradient of 4096 rows in 8 groups, N = 4096, K = 7168: 234 -> 206 us.
+__device__ __forceinline__ void in_strips(uint32_t tile, uint32_t rows, uint32_t cols, uint32_t& row, uint32_t& col) {
+  constexpr uint32_t H = 4;
+  const uint32_t strip = tile / (H * cols), at = tile - strip * H * cols, left = rows - strip * H, h = left < H ? left : H;
+  col = __builtin_amdgcn_readfirstlane(at / h);
+  row = __builtin_amdgcn_readfirstlane(strip * H + at - col * h);
+}
+
+// The row and column of a tile over all groups: the tall row tiles' first, so that a persistent grid
+// meets its cheap tiles last.
+__device__ __forceinline__ void tile_place(const RowTiles& n, uint32_t cols, uint32_t tile, uint32_t& row, uint32_t& col) {
+  const uint32_t tall = n.tall * cols;
+  if (tile < tall) {
+    in_strips(tile, n.tall, cols, row, col);
+  } else {
+    in_strips(tile - tall, n.all - n.tall, cols, row, col);
+    row += n.tall;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // One output tile
 // ---------------------------------------------------------------------------
+
+// A pointer that all lanes hold alike, in scalar registers.
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t u = (uint64_t)p;
+  return (const uint8_t*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u) |
+                          (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32);
+}
 
 // An operand of the tile in LDS: R rows (or columns) of the output by BK of the contraction.
 // ALONG: the contraction runs along memory; LDS rows are BK values, read 16 bytes a lane.
 // Else it runs across memory; LDS rows are the R values of one place in the contraction, and the
 // matrix instruction's operand is read transposed (ds_read_b64_tr_b16: sixteen lanes read four
 // places of sixteen values, lane i gets value i of the four).
-// PERM: the 32 columns of a block go to the instruction's rows in the order that leaves each lane
-// sixteen neighbouring columns of the result.
-template <int R, int BK, int NT, bool ALONG, bool PERM>
+template <int R, int BK, int NT, bool ALONG>
 struct Operand {
   static constexpr int CHUNKS = R * BK / 8;
   static constexpr int LOADS = CHUNKS / NT;
   static constexpr int BYTES = R * BK * 2;
   static constexpr int CPR = (ALONG ? BK : R) / 8;
   static_assert(CHUNKS % NT == 0, "every thread copies as much");
-  const uint16_t* src[LOADS];
-  int at[LOADS];                 // the chunk's place in the contraction
+  int tid;                       // thread of the tile
+  const uint8_t* base;           // of the tile's part of the operand, the same in all lanes
+  uint32_t off[LOADS];           // this lane's chunks from there, in bytes
 
   // 16-byte chunk c of LDS row `row` lies at c ^ swz(row): no bank conflicts in either kind of read
   // (across: the four places that sixteen lanes read lie in four different 64-byte columns).
@@ -155,49 +198,47 @@ struct Operand {
     else return 0;
   }
 
-  // Chunks of the operand whose contraction starts at `base`: rows (columns) [first, first + count)
-  // of the matrix exist; the tile's other ones repeat the last and their results are dropped.
-  __device__ __forceinline__ void setup(const uint16_t* base, int64_t ld, int64_t first, int64_t count) {
-    const int tid = threadIdx.x % NT;
+  // The contraction starts at `from`; rows (columns) [first, first + count) of the matrix exist, the
+  // tile's other ones repeat the last and their results are dropped.  Offsets stay below 2^32: ld is at
+  // most 2^23, rows of the tile 256.
+  __device__ __forceinline__ void setup(int thread, const uint16_t* from, int64_t ld, int64_t first, int64_t count) {
+    tid = thread;
+    base = (const uint8_t*)(from + (ALONG ? first * ld : first));
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const int q = i * NT + tid;
       const int row = q / CPR;
       const int c = (q % CPR) ^ swz(row);
-      if constexpr (ALONG) {
-        const int local = PERM ? (row & ~31) + 16 * ((row >> 2) & 1) + 4 * ((row & 31) >> 3) + (row & 3) : row;
-        const int64_t r = local < count ? local : count - 1;
-        src[i] = base + (first + r) * ld + c * 8;
-        at[i] = c * 8;
-      } else {
-        int64_t col = c * 8;
-        col = col < count ? col : count - 8;
-        src[i] = base + (int64_t)row * ld + first + col;
-        at[i] = row;
-      }
+      int64_t r = ALONG ? row : c * 8;
+      if (r >= count) r = ALONG ? count - 1 : count - 8;
+      off[i] = (uint32_t)((ALONG ? r * ld + c * 8 : row * ld + r) * 2);
     }
   }
 
-  // Copy i of contraction [k, k + BK) of n; zeros from n on (for both operands, so that nothing
-  // that lies there, a NaN included, reaches a sum).
+  // Copy i of contraction [k, k + BK) of n, WHOLE if that ends within n; else zeros from n on (for both
+  // operands, so that nothing that lies there, a NaN included, reaches a sum).
+  template <bool WHOLE>
   __device__ __forceinline__ void issue(int i, uint8_t* lds, int64_t k, int64_t n, int64_t ld) const {
-    const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x % NT) >> 6);
-    const void* p = src[i] + (ALONG ? k : k * ld);
-    if (k + BK > n && k + at[i] >= n) p = g_zero16;
-    copy16_to_lds(p, lds_addr(lds + (i * NT + wave * 64) * 16));
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint8_t* s = base + (ALONG ? k : k * ld) * 2;
+    const uint32_t to = lds_addr(lds + (i * NT + wave * 64) * 16);
+    if constexpr (WHOLE) {
+      copy16_to_lds(uniform(s), off[i], to);
+    } else {
+      const int q = i * NT + tid, row = q / CPR, at = ALONG ? (q % CPR ^ swz(row)) * 8 : row;
+      copy16_to_lds(k + at < n ? s + off[i] : g_zero16, to);
+    }
   }
 
-  // The instruction's operand: block b of 32, step ks of 16 along the contraction.
-  static __device__ __forceinline__ v8bf frag(const uint8_t* lds, int b, int ks) {
-    const int lane = threadIdx.x & 63;
+  // The instruction's operand: block b of 16, step ks of 32 along the contraction.
+  __device__ __forceinline__ v8bf frag(const uint8_t* lds, int b, int ks) const {
+    const int r = tid & 15, q = (tid & 63) >> 4;
     if constexpr (ALONG) {
-      const int row = 32 * b + (lane & 31);
-      return *(const v8bf*)(lds + row * (BK * 2) + (((2 * ks + (lane >> 5)) ^ swz(row)) * 16));
+      const int row = 16 * b + r;
+      return *(const v8bf*)(lds + row * (BK * 2) + (((4 * ks + q) ^ swz(row)) * 16));
     } else {
-      const int i = lane & 15, half = (lane >> 4) & 1, h = lane >> 5;
-      const int four = 4 * half + (i & 3);               // which four of the block's 32
-      const int piece = 8 * b + (PERM ? 4 * (four & 1) + (four >> 1) : four);
-      const int k = 16 * ks + 8 * h + (i >> 2);
+      const int piece = 4 * b + (r & 3);                 // four neighbouring values
+      const int k = 32 * ks + 8 * q + (r >> 2);
       const uint8_t* p = lds + k * (R * 2) + ((piece >> 1) ^ swz(k)) * 16 + (piece & 1) * 8;
       const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p));
       const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p + 4 * R * 2));
@@ -211,21 +252,30 @@ struct Operand {
 template <bool P_ALONG, bool Q_ALONG, int BM, int BN, int BK, int WM, int WN, int SP, int SQ>
 struct ProductTile {
   static constexpr int NT = WM * WN * 64;
-  static constexpr int FM = BM / WM / 32, FN = BN / WN / 32, KS = BK / 16;
-  typedef Operand<BM, BK, NT, P_ALONG, false> P;
-  typedef Operand<BN, BK, NT, Q_ALONG, true> Q;
+  static constexpr int FM = BM / WM / 16, FN = BN / WN / 16, KS = BK / 32;
+  typedef Operand<BM, BK, NT, P_ALONG> P;
+  typedef Operand<BN, BK, NT, Q_ALONG> Q;
   static constexpr int SMEM = SP * P::BYTES + SQ * Q::BYTES;
   static_assert(SP >= 2 && (SQ == SP || (SP == 2 && SQ == 3)), "the wait counts below");
   static_assert(KS % 2 == 0, "operands alternate between two sets of registers");
-  typedef v16f Acc[FM][FN];
+  typedef v4f Acc[FM][FN];   // lane (q, r) = (lane / 16, lane % 16): row r, columns 4 q .. 4 q + 3 of a block
 
   uint8_t* smem;
   P p;
   Q q;
 
+  // This thread's number in the tile, opaque: what follows from it is worked out for each tile, where a
+  // persistent kernel would else keep it in registers that the loop has no room for.
+  static __device__ __forceinline__ int thread() {
+    int tid = threadIdx.x % NT;
+    asm volatile("" : "+v"(tid));
+    __builtin_assume(tid >= 0 && tid < NT);
+    return tid;
+  }
+
   __device__ __forceinline__ uint8_t* pslot(int i) const { return smem + i * P::BYTES; }
   __device__ __forceinline__ uint8_t* qslot(int i) const { return smem + SP * P::BYTES + i * Q::BYTES; }
-  static __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((threadIdx.x % NT) >> 6); }
+  __device__ __forceinline__ int wave_id() const { return __builtin_amdgcn_readfirstlane(p.tid >> 6); }
   // A single wave orders its own copies and reads by its waits.
   static __device__ __forceinline__ void barrier() {
     if constexpr (NT > 64) block_barrier();
@@ -241,21 +291,22 @@ struct ProductTile {
 #pragma unroll
     for (int s = 0; s < (SP > SQ - 1 ? SP : SQ - 1); ++s) {
 #pragma unroll
-      for (int i = 0; s < SP && i < P::LOADS; ++i) p.issue(i, pslot(s), (int64_t)s * BK, n, ldp);
+      for (int i = 0; s < SP && i < P::LOADS; ++i) p.template issue<false>(i, pslot(s), (int64_t)s * BK, n, ldp);
 #pragma unroll
-      for (int i = 0; s < SQ - 1 && i < Q::LOADS; ++i) q.issue(i, qslot(s), (int64_t)s * BK, n, ldq);
+      for (int i = 0; s < SQ - 1 && i < Q::LOADS; ++i) q.template issue<false>(i, qslot(s), (int64_t)s * BK, n, ldq);
     }
     wait_vmcnt_le((SP - 1) * P::LOADS + (SQ - 2) * Q::LOADS);
     barrier();
     v8bf pf[2][FM], qf[2][FN];
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm) pf[0][fm] = P::frag(pslot(0), wm * FM + fm, 0);
+    for (int fm = 0; fm < FM; ++fm) pf[0][fm] = p.frag(pslot(0), wm * FM + fm, 0);
 #pragma unroll
-    for (int fn = 0; fn < FN; ++fn) qf[0][fn] = Q::frag(qslot(0), wn * FN + fn, 0);
+    for (int fn = 0; fn < FN; ++fn) qf[0][fn] = q.frag(qslot(0), wn * FN + fn, 0);
     constexpr int NM = FM * FN, NR = FM + FN;    // instructions and operands of a step
     constexpr int QS = KS - 1 < 2 ? KS - 1 : 2;  // steps over which Q's copies are spread
     int sp = 0, sq = 0;
-    for (int kt = 0; kt < nk; ++kt) {
+    const auto stage = [&](int kt, auto whole) __attribute__((always_inline)) {
+      constexpr bool WHOLE = decltype(whole)::value;
       const int np = sp == SP - 1 ? 0 : sp + 1, nq = sq == SQ - 1 ? 0 : sq + 1, bq = sq == 0 ? SQ - 1 : sq - 1;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -271,32 +322,37 @@ struct ProductTile {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < NM; ++i) {
-          const int fm = i / FN, fn = i % FN;
-          acc[fm][fn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[c][fn], pf[c][fm], acc[fm][fn], 0, 0, 0);
+          const int fm = i / FN, fn = fm & 1 ? FN - 1 - i % FN : i % FN;
+          acc[fm][fn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[c][fn], pf[c][fm], acc[fm][fn], 0, 0, 0);
           // the next step's operands (of the next stage in the last step; past the end they are read
           // from the ring all the same and not used)
 #pragma unroll
           for (int r = i * NR / NM; r < (i + 1) * NR / NM; ++r) {
             const int rk = last ? 0 : ks + 1;
-            if (r < FN) qf[d][r] = Q::frag(qslot(last ? nq : sq), wn * FN + r, rk);
-            else pf[d][r - FN] = P::frag(pslot(last ? np : sp), wm * FM + r - FN, rk);
+            if (r < FN) qf[d][r] = q.frag(qslot(last ? nq : sq), wn * FN + r, rk);
+            else pf[d][r - FN] = p.frag(pslot(last ? np : sp), wm * FM + r - FN, rk);
           }
           // P's copies into the slot that the last step has freed, Q's in the first steps after it
           if (last) {
 #pragma unroll
             for (int r = i * P::LOADS / NM; r < (i + 1) * P::LOADS / NM; ++r)
-              p.issue(r, pslot(sp), (int64_t)(kt + SP) * BK, n, ldp);
+              p.template issue<WHOLE>(r, pslot(sp), (int64_t)(kt + SP) * BK, n, ldp);
           } else if (ks < QS) {
 #pragma unroll
             for (int r = (ks * NM + i) * Q::LOADS / (QS * NM); r < (ks * NM + i + 1) * Q::LOADS / (QS * NM); ++r)
-              q.issue(r, qslot(bq), (int64_t)(kt + SQ - 1) * BK, n, ldq);
+              q.template issue<WHOLE>(r, qslot(bq), (int64_t)(kt + SQ - 1) * BK, n, ldq);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       sp = np;
       sq = nq;
-    }
+    };
+    // the copies that a stage issues are of whole stages while they lie before n
+    const int full = (int)(n / BK) - (SP > SQ - 1 ? SP : SQ - 1);
+    int kt = 0;
+    for (; kt < full; ++kt) stage(kt, std::true_type{});
+    for (; kt < nk; ++kt) stage(kt, std::false_type{});
     wait_vmcnt_le(0);                            // no copy is in flight when the ring is used again
   }
 
@@ -312,35 +368,28 @@ struct ProductTile {
     constexpr int PASSES = TILE <= SMEM ? 1 : TILE <= 2 * SMEM ? 2 : 4;
     constexpr int ROWS = BM / PASSES, FP = FM / PASSES;
     static_assert(ROWS * CPR * 16 <= SMEM && FM % PASSES == 0, "a pass fits the ring");
-    const int tid = threadIdx.x % NT, lane = tid & 63, h = lane >> 5, r32 = lane & 31;
+    const int tid = p.tid, r16 = tid & 15, q4 = (tid & 63) >> 4;
     const int wm = wave_id() / WN, wn = wave_id() % WN;
 #pragma unroll
     for (int ps = 0; ps < PASSES; ++ps) {
       barrier();
 #pragma unroll
       for (int f = 0; f < FP; ++f) {
-        const int r = (wm * FP + f) * 32 + r32;
+        const int r = (wm * FP + f) * 16 + r16;
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn) {
-          const v16f& x = acc[ps * FP + f][fn];
-#pragma unroll
-          for (int e = 0; e < 16 / PER; ++e) {
-            const int chunk = (wn * FN + fn) * (32 / PER) + h * (16 / PER) + e;
-            v4i v;
-            if constexpr (F32)
-              v = __builtin_bit_cast(v4i, v4f{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]});
-            else
-              v = v4i{(int)pack_bf16x2(x[8 * e], x[8 * e + 1]), (int)pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
-                      (int)pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), (int)pack_bf16x2(x[8 * e + 6], x[8 * e + 7])};
-            *(v4i*)(smem + (r * CPR + (chunk ^ (r & MASK))) * 16) = v;
-          }
+          const v4f& x = acc[ps * FP + f][fn];
+          const int col = (wn * FN + fn) * 16 + 4 * q4;
+          uint8_t* to = smem + (r * CPR + (col / PER ^ (r & MASK))) * 16;
+          if constexpr (F32) *(v4f*)to = x;
+          else *(v2i*)(to + col % PER * 2) = v2i{(int)pack_bf16x2(x[0], x[1]), (int)pack_bf16x2(x[2], x[3])};
         }
       }
       barrier();
 #pragma unroll 4
       for (int i = tid; i < ROWS * CPR; i += NT) {
         const int r = i / CPR, c = i % CPR;
-        const int64_t row = row0 + r / (32 * FP) * (32 * FM) + ps * FP * 32 + r % (32 * FP), col = col0 + PER * c;
+        const int64_t row = row0 + r / (16 * FP) * (16 * FM) + ps * FP * 16 + r % (16 * FP), col = col0 + PER * c;
         if (row >= row_end || col >= cols) continue;
         v4i v = *(const v4i*)(smem + (r * CPR + (c ^ (r & MASK))) * 16);
         v4i* o = (v4i*)((uint8_t*)out + (row * ldo + col) * (F32 ? 4 : 2));
@@ -360,9 +409,10 @@ template <typename E, bool Q_ALONG>
 __device__ __forceinline__ void product_tile(const ProductArgs& a, uint8_t* smem, const RowTile& t, int64_t col0) {
   E e;
   e.smem = smem;
-  e.p.setup(a.P, a.L, t.row0, t.row_end - t.row0);
+  const int tid = E::thread();
+  e.p.setup(tid, a.P, a.L, t.row0, t.row_end - t.row0);
   const int64_t ldq = Q_ALONG ? a.L : a.C;
-  e.q.setup(a.Q + t.g * a.L * a.C, ldq, col0, a.C - col0);
+  e.q.setup(tid, a.Q + t.g * a.L * a.C, ldq, col0, a.C - col0);
   typename E::Acc acc = {};
   e.run(a.L, a.L, ldq, acc);
   e.template store<false>(a.out, a.C, t.row0, t.row_end, col0, a.C, false, acc);
@@ -374,10 +424,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) product_kernel(ProductArgs a)
   typedef ProductTile<true, Q_ALONG, BM, BN, BK, WM, WN, SP, SQ> E;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[E::SMEM];
   const RowTiles n = count_row_tiles<BM>(a);
-  const int64_t T = (int64_t)n.all * a.col_tiles;
-  if ((int64_t)blockIdx.x >= T) return;
-  const int64_t slot = xcd_slot(blockIdx.x, T);
-  product_tile<E, Q_ALONG>(a, smem, find_row_tile<BM>(a, n, (uint32_t)(slot / a.col_tiles)), slot % a.col_tiles * BN);
+  const uint32_t T = n.all * a.col_tiles;
+  if (blockIdx.x >= T) return;
+  uint32_t row, col;
+  tile_place(n, a.col_tiles, xcd_slot32(blockIdx.x, T), row, col);
+  product_tile<E, Q_ALONG>(a, smem, find_row_tile<BM>(a, n, row), (int64_t)col * BN);
 }
 
 // One workgroup per compute unit; the tiles that do not fill a whole round of them are computed
@@ -389,23 +440,27 @@ __global__ void __launch_bounds__(512, 2) product_persistent_kernel(ProductArgs 
   typedef ProductTile<true, Q_ALONG, BM / 2, BN / 2, 64, 2, 4, 5, 5> H;
   static_assert(H::SMEM <= E::SMEM, "quarters share the ring");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[E::SMEM];
-  const int64_t P = gridDim.x, w = xcd_slot(blockIdx.x, P);
+  const uint32_t P = gridDim.x, w = xcd_slot32(blockIdx.x, P);
   const RowTiles n = count_row_tiles<BM>(a);
-  const int64_t T = (int64_t)n.all * a.col_tiles, tall = (int64_t)n.tall * a.col_tiles;
+  const uint32_t T = n.all * a.col_tiles, tall = n.tall * a.col_tiles;
   // of the last tiles, those with more than half the rows have four quarters, the others two
-  int64_t whole = T / P * P;
-  const int64_t four = tall > whole ? tall - whole : 0, two = T - whole - four;
-  const int64_t quarters = 4 * four + 2 * two;
+  uint32_t whole = T / P * P;
+  const uint32_t four = tall > whole ? tall - whole : 0, two = T - whole - four;
+  const uint32_t quarters = 4 * four + 2 * two;
   if (quarters > 2 * P) whole = T;
-  for (int64_t tile = w; tile < whole; tile += P)
-    product_tile<E, Q_ALONG>(a, smem, find_row_tile<BM>(a, n, (uint32_t)(tile / a.col_tiles)), tile % a.col_tiles * BN);
+  uint32_t row, col;
+  for (uint32_t tile = w; tile < whole; tile += P) {
+    tile_place(n, a.col_tiles, tile, row, col);
+    product_tile<E, Q_ALONG>(a, smem, find_row_tile<BM>(a, n, row), (int64_t)col * BN);
+  }
   if (whole == T) return;
-  for (int64_t i = w; i < quarters; i += P) {
-    const int64_t tile = whole + (i < 4 * four ? i / 4 : four + (i - 4 * four) / 2);
-    const int part = (int)(i < 4 * four ? i % 4 : (i - 4 * four) % 2);
-    RowTile t = find_row_tile<BM>(a, n, (uint32_t)(tile / a.col_tiles));
+  for (uint32_t i = w; i < quarters; i += P) {
+    const bool tallest = i < 4 * four;
+    const uint32_t at = tallest ? i : i - 4 * four, part = tallest ? at % 4 : at % 2;
+    tile_place(n, a.col_tiles, whole + (tallest ? at / 4 : four + at / 2), row, col);
+    RowTile t = find_row_tile<BM>(a, n, row);
     t.row0 += part / 2 * (BM / 2);
-    const int64_t col0 = tile % a.col_tiles * BN + part % 2 * (BN / 2);
+    const int64_t col0 = (int64_t)col * BN + part % 2 * (BN / 2);
     if (t.row0 < t.row_end && col0 < a.C) product_tile<H, Q_ALONG>(a, smem, t, col0);
   }
 }
@@ -414,16 +469,17 @@ __global__ void __launch_bounds__(512, 2) product_persistent_kernel(ProductArgs 
 // and their sums are added in the order of the waves.
 template <bool Q_ALONG, int BN, int BK, int W, int SLOTS>
 __global__ void __launch_bounds__(W * 64) product_split_kernel(ProductArgs a) {
-  constexpr int BM = 32, FN = BN / 32;
+  constexpr int BM = 32, FM = 2, FN = BN / 16;
   typedef ProductTile<true, Q_ALONG, BM, BN, BK, 1, 1, SLOTS, SLOTS> E;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[W * E::SMEM];
   static_assert(BM * BN * 4 <= E::SMEM, "a wave's sums fit its ring");
   const RowTiles n = count_row_tiles<BM>(a);
-  const int64_t T = (int64_t)n.all * a.col_tiles;
-  if ((int64_t)blockIdx.x >= T) return;
-  const int64_t slot = xcd_slot(blockIdx.x, T);
-  const RowTile t = find_row_tile<BM>(a, n, (uint32_t)(slot / a.col_tiles));
-  const int64_t col0 = slot % a.col_tiles * BN;
+  const uint32_t T = n.all * a.col_tiles;
+  if (blockIdx.x >= T) return;
+  uint32_t row_tile, col_tile;
+  tile_place(n, a.col_tiles, xcd_slot32(blockIdx.x, T), row_tile, col_tile);
+  const RowTile t = find_row_tile<BM>(a, n, row_tile);
+  const int64_t col0 = (int64_t)col_tile * BN;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t per = ((a.L + W - 1) / W + BK - 1) / BK * BK;
   const int64_t k0 = wave * per, k1 = k0 + per < a.L ? k0 + per : a.L;
@@ -432,30 +488,28 @@ __global__ void __launch_bounds__(W * 64) product_split_kernel(ProductArgs a) {
   const int64_t ldq = Q_ALONG ? a.L : a.C;
   typename E::Acc acc = {};
   if (k0 < k1) {
-    e.p.setup(a.P + k0, a.L, t.row0, t.row_end - t.row0);
-    e.q.setup(a.Q + t.g * a.L * a.C + (Q_ALONG ? k0 : k0 * a.C), ldq, col0, a.C - col0);
+    const int tid = E::thread();
+    e.p.setup(tid, a.P + k0, a.L, t.row0, t.row_end - t.row0);
+    e.q.setup(tid, a.Q + t.g * a.L * a.C + (Q_ALONG ? k0 : k0 * a.C), ldq, col0, a.C - col0);
     e.run(k1 - k0, a.L, ldq, acc);
   }
-  // lane (h, r) holds row r, columns 32 fn + 16 h + i
 #pragma unroll
-  for (int fn = 0; fn < FN; ++fn)
+  for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *((v4f*)e.smem + (fn * 4 + i) * 64 + lane) =
-          v4f{acc[0][fn][4 * i], acc[0][fn][4 * i + 1], acc[0][fn][4 * i + 2], acc[0][fn][4 * i + 3]};
+    for (int fn = 0; fn < FN; ++fn) *((v4f*)e.smem + (fm * FN + fn) * 64 + lane) = acc[fm][fn];
   __syncthreads();
   // a thread: eight neighbouring columns of one row
   for (int i = threadIdx.x; i < BM * BN / 8; i += W * 64) {
     const int r = i / (BN / 8), c = i % (BN / 8);
     const int64_t row = t.row0 + r, col = col0 + 8 * c;
     if (row >= t.row_end || col >= a.C) continue;
-    const int from = (c / 4 * 4 + c % 2 * 2) * 64 + c / 2 % 2 * 32 + r;   // fn = c / 4, h = c / 2 % 2, i = 2 (c % 2)
+    const int from = (r / 16 * FN + c / 2) * 64 + c % 2 * 32 + r % 16;   // its first four columns; the others 16 lanes on
     v4f lo = {0.f, 0.f, 0.f, 0.f}, hi = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const v4f* s = (const v4f*)(smem + w * E::SMEM) + from;
       lo += s[0];
-      hi += s[64];
+      hi += s[16];
     }
     store_out((v4i*)((uint16_t*)a.out + row * a.C + col),
               v4i{(int)pack_bf16x2(lo.x, lo.y), (int)pack_bf16x2(lo.z, lo.w), (int)pack_bf16x2(hi.x, hi.y),
@@ -473,16 +527,17 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) wgrad_kernel(ProductArgs a) {
   typedef ProductTile<false, false, BM, BN, BK, WM, WN, SP, SQ> E;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[E::SMEM];
   // every XCD takes an eighth of each group's tiles: groups differ in size
-  const int64_t per = a.row_tiles * a.col_tiles * a.splits, share = (per + 7) / 8;
-  const int64_t i = blockIdx.x / 8;
-  int64_t tile = blockIdx.x % 8 * share + i % share;
+  const uint32_t per = a.row_tiles * a.col_tiles * a.splits, share = (per + 7) / 8;
+  const uint32_t i = blockIdx.x / 8;
+  uint32_t tile = blockIdx.x % 8 * share + i % share;
   if (tile >= per) return;
   int g = (int)(i / share);
   int64_t first, count;
   nth_group(a, g, first, count);
   const int64_t part = tile % a.splits;
-  tile /= a.splits;
-  const int64_t row0 = tile / a.col_tiles * BM, col0 = tile % a.col_tiles * BN;
+  uint32_t row, col;
+  in_strips(tile / a.splits, a.row_tiles, a.col_tiles, row, col);
+  const int64_t row0 = (int64_t)row * BM, col0 = (int64_t)col * BN;
   void* out = (uint8_t*)a.out + (int64_t)g * a.L * a.C * (F32 ? 4 : 2);
   if (a.splits > 1) {
     const int64_t rows = ((count + a.splits - 1) / a.splits + BK - 1) / BK * BK;
@@ -493,8 +548,9 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) wgrad_kernel(ProductArgs a) {
   }
   E e;
   e.smem = smem;
-  e.p.setup(a.P + first * a.L, a.L, row0, a.L - row0);
-  e.q.setup(a.Q + first * a.C, a.C, col0, a.C - col0);
+  const int tid = E::thread();
+  e.p.setup(tid, a.P + first * a.L, a.L, row0, a.L - row0);
+  e.q.setup(tid, a.Q + first * a.C, a.C, col0, a.C - col0);
   if (F32 && a.splits == 1 && a.accumulate && count == 0) return;
   typename E::Acc acc = {};
   e.run(count, a.L, a.C, acc);
@@ -531,7 +587,7 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(ProductArgs a) {
 
 namespace {
 
-constexpr int64_t kWgradRows = 256, kWgradCols = 128;
+constexpr int64_t kWgradRows = 256, kWgradCols = 256;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -556,7 +612,7 @@ hipError_t launch_rows(ProductArgs a, int cus, hipStream_t stream) {
       a.col_tiles = cdiv(a.C, BN);
       const dim3 grid((uint32_t)(most_row_tiles(a, 32) * a.col_tiles));
       if constexpr (Q_ALONG) hipLaunchKernelGGL((product_split_kernel<true, 32, 64, 4, 4>), grid, dim3(256), 0, stream, a);
-      else hipLaunchKernelGGL((product_split_kernel<false, 64, 32, 8, 3>), grid, dim3(512), 0, stream, a);
+      else hipLaunchKernelGGL((product_split_kernel<false, 64, 64, 4, 3>), grid, dim3(256), 0, stream, a);
       break;
     }
     case kRows32:
@@ -610,8 +666,8 @@ hipError_t launch_wgrad(bool f32, ProductArgs a, hipStream_t stream) {
   a.col_tiles = cdiv(a.C, kWgradCols);
   a.splits = wgrad_splits(a.G, a.M, a.L, a.C);
   const dim3 grid((uint32_t)wgrad_grid(a));
-  if (f32 || a.splits > 1) hipLaunchKernelGGL((wgrad_kernel<true, 256, 128, 32, 2, 2, 3, 3>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((wgrad_kernel<false, 256, 128, 32, 2, 2, 3, 3>), grid, dim3(256), 0, stream, a);
+  if (f32 || a.splits > 1) hipLaunchKernelGGL((wgrad_kernel<true, 256, 256, 64, 2, 4, 2, 3>), grid, dim3(512), 0, stream, a);
+  else hipLaunchKernelGGL((wgrad_kernel<false, 256, 256, 64, 2, 4, 2, 3>), grid, dim3(512), 0, stream, a);
   if (a.splits > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -68,6 +68,12 @@ __device__ __forceinline__ void copy16_to_lds(const void* src, uint32_t lds_base
                :: "v"(src), "s"(__builtin_amdgcn_readfirstlane(lds_base)) : "memory");
 }
 
+// Same from a base that all lanes share and a byte offset per lane.
+__device__ __forceinline__ void copy16_to_lds(const void* base, uint32_t off, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds_base)) : "memory");
+}
+
 // Same with the non-temporal hint, for data that one workgroup reads once (the
 // weights of a small-M call): it streams past the caches instead of displacing
 // what other workgroups reuse.

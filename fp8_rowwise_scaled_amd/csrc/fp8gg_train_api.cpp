@@ -33,13 +33,14 @@ fp8gg_status check_product(int64_t G, int64_t M, int64_t N, int64_t K) {
                 (long long)N, (long long)K);
   if (N % 8 != 0 || K % 8 != 0)
     return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "N=%lld and K=%lld must be multiples of 8", (long long)N, (long long)K);
-  if (G > kMaxDim || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+  // N and K: the kernels' offsets within 256 rows have 32 bits
+  if (G > kMaxDim || M > kMaxDim || N > (1 << 23) || K > (1 << 23))
     return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "G=%lld total_M=%lld N=%lld K=%lld is too large", (long long)G, (long long)M,
                 (long long)N, (long long)K);
-  // tensors below 2^48 bytes
+  // tensors of at most 2^47 bytes
   const double most = std::ldexp(1.0, 46);
   if ((double)M * N > most || (double)M * K > most || (double)G * N * K > most)
-    return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "a tensor of G=%lld total_M=%lld N=%lld K=%lld exceeds 2^48 bytes", (long long)G,
+    return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "a tensor of G=%lld total_M=%lld N=%lld K=%lld exceeds 2^47 bytes", (long long)G,
                 (long long)M, (long long)N, (long long)K);
   return FP8GG_OK;
 }

@@ -22,8 +22,8 @@ struct ProductArgs {
   float* partial;                 // [splits, G, L, C], splits > 1 only
   int32_t accumulate;
   // set by the launcher
-  int32_t splits;
-  int64_t row_tiles, col_tiles;
+  uint32_t splits;
+  uint32_t row_tiles, col_tiles;
 };
 
 struct WeightBlocksArgs {

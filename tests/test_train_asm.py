@@ -8,7 +8,7 @@ from tests.test_kernel_asm import device_asm, m0_uses_outside_lds_copies
 
 def test_products_use_m0_only_for_the_lds_copies(tmp_path):
     asm = device_asm(tmp_path, os.path.join(B.CSRC, "fp8gg_bf16.hip"))
-    assert "global_load_lds" in asm and "ds_read_b64_tr_b16" in asm and "v_mfma_f32_32x32x16_bf16" in asm
+    assert "global_load_lds" in asm and "ds_read_b64_tr_b16" in asm and "v_mfma_f32_16x16x32_bf16" in asm
     uses = m0_uses_outside_lds_copies(asm)
     assert not uses, f"M0 used outside the LDS copies: {uses[:5]}"
 
