@@ -281,6 +281,10 @@ struct ProductTile {
     if constexpr (NT > 64) block_barrier();
     else asm volatile("" ::: "memory");
   }
+  static __device__ __forceinline__ void publish() {
+    if constexpr (NT > 64) publish_barrier();
+    else asm volatile("" ::: "memory");
+  }
 
   // acc += the products over a contraction of n.
   __device__ __forceinline__ void run(int64_t n, int64_t ldp, int64_t ldq, Acc& acc) const {
@@ -385,7 +389,7 @@ struct ProductTile {
           else *(v2i*)(to + col % PER * 2) = v2i{(int)pack_bf16x2(x[0], x[1]), (int)pack_bf16x2(x[2], x[3])};
         }
       }
-      barrier();
+      publish();
 #pragma unroll 4
       for (int i = tid; i < ROWS * CPR; i += NT) {
         const int r = i / CPR, c = i % CPR;

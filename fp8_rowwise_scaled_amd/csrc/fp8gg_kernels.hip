@@ -743,7 +743,7 @@ struct LdsTile {
         *(v4i*)(smem + (r * CHUNKS_PER_ROW + (chunk ^ (r & SHUF_MASK))) * 16) = pk[fm][s >> 1][s & 1];
       }
     }
-    block_barrier();
+    publish_barrier();
     const int64_t N = a.N;
     const int64_t cend = tile_col_end(a, t);
 #pragma unroll 4

@@ -92,10 +92,19 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(lds_ptr_t)p;
 }
 
+// Orders the waves of a workgroup, and waits for nothing: what they have copied or written they wait for
+// themselves before it.
 __device__ __forceinline__ void block_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// ... after each wave's own LDS operations are done: what one has written, the others read after it.
+__device__ __forceinline__ void publish_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt 0, the other counters left alone
+  block_barrier();
 }
 
 // Tile order across the XCDs.  MI355X dispatches consecutive workgroups of a grid
