@@ -61,6 +61,9 @@ __device__ __forceinline__ void group_rows(const ProductArgs& a, int g0, uint32_
   start = lane ? before : rows;
 }
 
+// The stores' cache policy: written once, past the caches.
+constexpr int kPastCaches = 2;
+
 struct RowTile {
   int g;
   int64_t row0, row_end;
@@ -107,31 +110,6 @@ __device__ __forceinline__ RowTile find_row_tile(const ProductArgs& a, const Row
     rows = lane_value(end, 63);
   }
   return {0, 0, 0};
-}
-
-// Rows of one group, and (up to 64 groups) the group that comes nth when they are taken by size,
-// the largest first.
-__device__ __forceinline__ void nth_group(const ProductArgs& a, int& g, int64_t& first, int64_t& count) {
-  uint32_t rows = 0, start, end;
-  if (a.G <= 64) {
-    group_rows(a, 0, 0, start, end);
-    const int lane = threadIdx.x & 63;
-    const uint32_t mine = end - start;
-    int rank = 0;
-    for (int o = 0; o < (int)a.G; ++o) {
-      const uint32_t other = lane_value(mine, o);
-      rank += other > mine || (other == mine && o < lane);
-    }
-    g = __builtin_ctzll(__ballot(lane < a.G && rank == g));
-  } else {
-    for (int g0 = 0;; g0 += 64) {
-      group_rows(a, g0, rows, start, end);
-      if (g < g0 + 64) break;
-      rows = lane_value(end, 63);
-    }
-  }
-  first = lane_value(start, g & 63);
-  count = lane_value(end, g & 63) - first;
 }
 
 // xcd_slot in 32 bits (the launcher's bound on the tiles).
@@ -286,21 +264,41 @@ struct ProductTile {
     else asm volatile("" ::: "memory");
   }
 
-  // acc += the products over a contraction of n.
-  __device__ __forceinline__ void run(int64_t n, int64_t ldp, int64_t ldq, Acc& acc) const {
-    const int wm = wave_id() / WN, wn = wave_id() % WN;
-    const int nk = (int)((n + BK - 1) / BK);
-    barrier();                                   // the last tile's reads of the ring are done
-    if (nk == 0) return;
+  // Copies of the first stages of a contraction of n: all that the loop starts with, or in two parts, HEAD (all
+  // of P's, Q's first) and REST.  No wave reads their slots any more.
+  enum Part { ALL, HEAD, REST };
+  template <Part PART = ALL>
+  __device__ __forceinline__ void prologue(int64_t n, int64_t ldp, int64_t ldq) const {
+    if (n <= 0) return;
+    constexpr int Q0 = PART == REST ? 1 : 0, Q1 = PART == HEAD ? 1 : SQ - 1;
 #pragma unroll
     for (int s = 0; s < (SP > SQ - 1 ? SP : SQ - 1); ++s) {
 #pragma unroll
-      for (int i = 0; s < SP && i < P::LOADS; ++i) p.template issue<false>(i, pslot(s), (int64_t)s * BK, n, ldp);
+      for (int i = 0; PART != REST && s < SP && i < P::LOADS; ++i) p.template issue<false>(i, pslot(s), (int64_t)s * BK, n, ldp);
 #pragma unroll
-      for (int i = 0; s < SQ - 1 && i < Q::LOADS; ++i) q.template issue<false>(i, qslot(s), (int64_t)s * BK, n, ldq);
+      for (int i = 0; s >= Q0 && s < Q1 && i < Q::LOADS; ++i) q.template issue<false>(i, qslot(s), (int64_t)s * BK, n, ldq);
     }
-    wait_vmcnt_le((SP - 1) * P::LOADS + (SQ - 2) * Q::LOADS);
+  }
+
+  // acc += the products over a contraction of n, after its prologue.  YOUNGER: only its HEAD is under way, and
+  // behind it, if `younger`, so many stores of each wave, which read from the slots of the REST.
+  template <int YOUNGER = 0>
+  __device__ __forceinline__ void loop(int64_t n, int64_t ldp, int64_t ldq, bool younger, Acc& acc) const {
+    constexpr bool HEADED = YOUNGER > 0;
+    const int wm = wave_id() / WN, wn = wave_id() % WN;
+    const int nk = (int)((n + BK - 1) / BK);
+    asm volatile("" ::: "memory");               // whatever came before is issued before the waits below
+    if (nk == 0) {
+      barrier();                                 // the waves part here as after the loop
+      return;
+    }
+    constexpr int FIRST = (SP - 1) * P::LOADS + (HEADED ? 0 : (SQ - 2) * Q::LOADS);
+    constexpr int NEXT = SP == SQ ? (SP - 2) * (P::LOADS + Q::LOADS) : Q::LOADS;
+    static_assert(!HEADED || (SP == 2 && SQ == 3), "HEAD: P's two stages and Q's first");
+    if (younger) wait_vmcnt_le(FIRST + YOUNGER);
+    else wait_vmcnt_le(FIRST);
     barrier();
+    if constexpr (HEADED) prologue<REST>(n, ldp, ldq);
     v8bf pf[2][FM], qf[2][FN];
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm) pf[0][fm] = p.frag(pslot(0), wm * FM + fm, 0);
@@ -320,7 +318,7 @@ struct ProductTile {
           // this wave has read its last operands of stage kt, and stage kt + 1 has landed once only
           // the younger copies are outstanding; the barrier says so of all waves
           __builtin_amdgcn_s_waitcnt(0xC07F);    // lgkmcnt 0
-          wait_vmcnt_le(SP == SQ ? (SP - 2) * (P::LOADS + Q::LOADS) : Q::LOADS);
+          wait_vmcnt_le(NEXT);
           barrier();
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -357,26 +355,72 @@ struct ProductTile {
     int kt = 0;
     for (; kt < full; ++kt) stage(kt, std::true_type{});
     for (; kt < nk; ++kt) stage(kt, std::false_type{});
-    wait_vmcnt_le(0);                            // no copy is in flight when the ring is used again
+    // No copy is in flight, of any wave's, when the ring is used again.  (Past the end a wave may still be
+    // reading operands that nothing uses.)
+    wait_vmcnt_le(0);
+    barrier();
   }
 
-  // Rows [row0, row_end) and columns [col0, cols) of the output through the idle ring, so that every
-  // store covers whole rows of the tile, as many rows at a time as the ring holds.  F32: the output's
-  // type; else bf16, rounded to nearest even from the fp32 sum.
-  template <bool F32>
-  __device__ __forceinline__ void store(void* out, int64_t ldo, int64_t row0, int64_t row_end, int64_t col0, int64_t cols,
-                                        bool accumulate, const Acc& acc) const {
-    constexpr int PER = F32 ? 4 : 8;             // values of a 16-byte chunk
-    constexpr int CPR = BN / PER, MASK = (CPR < 16 ? CPR : 16) - 1;
-    constexpr int TILE = BM * BN * (F32 ? 4 : 2);
-    constexpr int PASSES = TILE <= SMEM ? 1 : TILE <= 2 * SMEM ? 2 : 4;
-    constexpr int ROWS = BM / PASSES, FP = FM / PASSES;
-    static_assert(ROWS * CPR * 16 <= SMEM && FM % PASSES == 0, "a pass fits the ring");
+  __device__ __forceinline__ void run(int64_t n, int64_t ldp, int64_t ldq, Acc& acc) const {
+    prologue(n, ldp, ldq);
+    loop(n, ldp, ldq, false, acc);
+  }
+
+  // Rows [row0, row_end) and columns [col0, cols) of a bf16 output, rounded to nearest even from the fp32
+  // sums, through the idle ring, so that every store covers whole rows of the tile.
+  __device__ __forceinline__ void store(uint16_t* out, int64_t ldo, int64_t row0, int64_t row_end, int64_t col0, int64_t cols,
+                                        const Acc& acc) const {
+    constexpr int CPR = BN / 8, MASK = (CPR < 16 ? CPR : 16) - 1;
+    static_assert(BM * BN * 2 <= SMEM, "the tile fits the ring");
     const int tid = p.tid, r16 = tid & 15, q4 = (tid & 63) >> 4;
     const int wm = wave_id() / WN, wn = wave_id() % WN;
 #pragma unroll
-    for (int ps = 0; ps < PASSES; ++ps) {
-      barrier();
+    for (int fm = 0; fm < FM; ++fm) {
+      const int r = (wm * FM + fm) * 16 + r16;
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) {
+        const v4f& x = acc[fm][fn];
+        const int col = (wn * FN + fn) * 16 + 4 * q4;
+        *(v2i*)(smem + (r * CPR + (col / 8 ^ (r & MASK))) * 16 + col % 8 * 2) =
+            v2i{(int)pack_bf16x2(x[0], x[1]), (int)pack_bf16x2(x[2], x[3])};
+      }
+    }
+    publish();
+#pragma unroll 4
+    for (int i = tid; i < BM * CPR; i += NT) {
+      const int r = i / CPR, c = i % CPR;
+      if (row0 + r < row_end && col0 + 8 * c < cols)
+        store_out((v4i*)(out + (row0 + r) * ldo + col0 + 8 * c), *(const v4i*)(smem + (r * CPR + (c ^ (r & MASK))) * 16));
+    }
+    barrier();                                   // the ring is free again
+  }
+
+  // The same while the HEAD of the next tile's prologue is under way, through the rest of the ring (Q's last two
+  // slots), as many rows at a time as that holds.  Whole rows count: each wave by itself, without barriers but
+  // 256 bytes of a row at a time, takes 357 us instead of 342 for the gate and up weights' gradient, and
+  // straight from the registers, 64 bytes at a time, it took 366 instead of 309.  F32: the output's type, else
+  // bf16.  What lies outside is sent past the buffer's end, which drops it, so that every wave issues the same
+  // number of stores, STORES.
+  template <bool F32>
+  static constexpr int PASSES = BM * BN * (F32 ? 4 : 2) / (2 * Q::BYTES);
+  template <bool F32>
+  static constexpr int STORES = BM * BN * (F32 ? 4 : 2) / 16 / NT;
+  template <bool F32>
+  __device__ __forceinline__ void store_behind(void* out, int64_t ldo, int64_t row0, int64_t row_end, int64_t col0, int64_t cols,
+                                               bool accumulate, const Acc& acc) const {
+    constexpr int SIZE = F32 ? 4 : 2, PER = 16 / SIZE;   // values of a 16-byte chunk
+    constexpr int CPR = BN / PER, MASK = (CPR < 16 ? CPR : 16) - 1;
+    constexpr int ROWS = BM / PASSES<F32>, FP = FM / PASSES<F32>, PART = ROWS * CPR / NT;
+    static_assert(FM % PASSES<F32> == 0 && ROWS * CPR % NT == 0, "whole blocks a pass, as much for every thread");
+    constexpr uint32_t kEnd = 0xFFFFFFF0u;       // past every offset within 256 rows of 2^22 values
+    uint8_t* const lds = qslot(SQ - 2);
+    const int tid = p.tid, r16 = tid & 15, q4 = (tid & 63) >> 4;
+    const int wm = wave_id() / WN, wn = wave_id() % WN;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((uint8_t*)out + (row0 * ldo + col0) * SIZE, 0, kEnd, 0x00020000);
+    const int64_t rows_left = row_end - row0, cols_left = cols - col0;
+#pragma unroll
+    for (int ps = 0; ps < PASSES<F32>; ++ps) {
+      if (ps > 0) barrier();
 #pragma unroll
       for (int f = 0; f < FP; ++f) {
         const int r = (wm * FP + f) * 16 + r16;
@@ -384,22 +428,23 @@ struct ProductTile {
         for (int fn = 0; fn < FN; ++fn) {
           const v4f& x = acc[ps * FP + f][fn];
           const int col = (wn * FN + fn) * 16 + 4 * q4;
-          uint8_t* to = smem + (r * CPR + (col / PER ^ (r & MASK))) * 16;
+          uint8_t* to = lds + (r * CPR + (col / PER ^ (r & MASK))) * 16;
           if constexpr (F32) *(v4f*)to = x;
           else *(v2i*)(to + col % PER * 2) = v2i{(int)pack_bf16x2(x[0], x[1]), (int)pack_bf16x2(x[2], x[3])};
         }
       }
       publish();
-#pragma unroll 4
-      for (int i = tid; i < ROWS * CPR; i += NT) {
-        const int r = i / CPR, c = i % CPR;
-        const int64_t row = row0 + r / (16 * FP) * (16 * FM) + ps * FP * 16 + r % (16 * FP), col = col0 + PER * c;
-        if (row >= row_end || col >= cols) continue;
-        v4i v = *(const v4i*)(smem + (r * CPR + (c ^ (r & MASK))) * 16);
-        v4i* o = (v4i*)((uint8_t*)out + (row * ldo + col) * (F32 ? 4 : 2));
+#pragma unroll
+      for (int i = 0; i < PART; ++i) {
+        const int at = i * NT + tid, r = at / CPR, c = at % CPR;
+        const int row = r / (16 * FP) * (16 * FM) + ps * FP * 16 + r % (16 * FP), col = PER * c;
+        const uint32_t off = row < rows_left && col < cols_left ? (uint32_t)((row * ldo + col) * SIZE) : kEnd;
+        u32x4 v = *(const u32x4*)(lds + (r * CPR + (c ^ (r & MASK))) * 16);
         if constexpr (F32)
-          if (accumulate) v = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, v) + __builtin_bit_cast(v4f, *o));
-        store_out(o, v);
+          if (accumulate)
+            v = __builtin_bit_cast(u32x4, __builtin_bit_cast(v4f, v) +
+                                              __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0)));
+        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, off, 0, kPastCaches);
       }
     }
   }
@@ -419,7 +464,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, uint8_t* smem
   e.q.setup(tid, a.Q + t.g * a.L * a.C, ldq, col0, a.C - col0);
   typename E::Acc acc = {};
   e.run(a.L, a.L, ldq, acc);
-  e.template store<false>(a.out, a.C, t.row0, t.row_end, col0, a.C, false, acc);
+  e.store((uint16_t*)a.out, a.C, t.row0, t.row_end, col0, a.C, acc);
 }
 
 // One tile per workgroup; workgroups past the last tile end at once.
@@ -525,40 +570,116 @@ __global__ void __launch_bounds__(W * 64) product_split_kernel(ProductArgs a) {
 // The weights' gradient: the contraction runs over a group's rows
 // ---------------------------------------------------------------------------
 
-// a.splits > 1: the group's rows in so many parts, each part's sums to a.partial.
-template <bool F32, int BM, int BN, int BK, int WM, int WN, int SP, int SQ>
-__global__ void __launch_bounds__(WM * WN * 64, 2) wgrad_kernel(ProductArgs a) {
-  typedef ProductTile<false, false, BM, BN, BK, WM, WN, SP, SQ> E;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[E::SMEM];
-  // every XCD takes an eighth of each group's tiles: groups differ in size
-  const uint32_t per = a.row_tiles * a.col_tiles * a.splits, share = (per + 7) / 8;
-  const uint32_t i = blockIdx.x / 8;
-  uint32_t tile = blockIdx.x % 8 * share + i % share;
-  if (tile >= per) return;
-  int g = (int)(i / share);
-  int64_t first, count;
-  nth_group(a, g, first, count);
-  const int64_t part = tile % a.splits;
-  uint32_t row, col;
-  in_strips(tile / a.splits, a.row_tiles, a.col_tiles, row, col);
-  const int64_t row0 = (int64_t)row * BM, col0 = (int64_t)col * BN;
-  void* out = (uint8_t*)a.out + (int64_t)g * a.L * a.C * (F32 ? 4 : 2);
-  if (a.splits > 1) {
-    const int64_t rows = ((count + a.splits - 1) / a.splits + BK - 1) / BK * BK;
-    const int64_t from = part * rows < count ? part * rows : count;
-    first += from;
-    count = rows < count - from ? rows : count - from;
-    out = (float*)a.partial + (part * a.G + g) * a.L * a.C;
+// The groups' rows, one group per lane, kept over a workgroup's tiles: up to 64 groups by size, the largest
+// first, else the 64 from g0 on in their own order.
+struct GroupTable {
+  uint32_t g, first, count;      // of this lane's group
+  int64_t g0;
+  uint32_t rows;                 // before group g0
+
+  __device__ __forceinline__ void load(const ProductArgs& a) {
+    uint32_t end;
+    group_rows(a, (int)g0, rows, first, end);
+    g = (uint32_t)g0 + (threadIdx.x & 63);
+    count = end - first;
   }
+  __device__ __forceinline__ void start(const ProductArgs& a) {
+    g0 = 0;
+    rows = 0;
+    load(a);
+    if (a.G > 64) return;
+    const int lane = threadIdx.x & 63;
+    int rank = 0;
+    for (int o = 0; o < 64; ++o) {
+      const uint32_t other = lane_value(count, o);
+      rank += other > count || (other == count && o < lane);
+    }
+    g = (uint32_t)__builtin_amdgcn_ds_permute(rank * 4, (int)g);
+    first = (uint32_t)__builtin_amdgcn_ds_permute(rank * 4, (int)first);
+    count = (uint32_t)__builtin_amdgcn_ds_permute(rank * 4, (int)count);
+  }
+  // The nth group; n never falls from one call to the next.
+  __device__ __forceinline__ void nth(const ProductArgs& a, int64_t n, int64_t& group, int64_t& from, int64_t& many) {
+    while (n >= g0 + 64) {
+      rows = lane_value(first + count, 63);
+      g0 += 64;
+      load(a);
+    }
+    const int l = (int)(n - g0);
+    group = lane_value(g, l);
+    from = lane_value(first, l);
+    many = lane_value(count, l);
+  }
+};
+
+// One workgroup per compute unit.  Every XCD takes an eighth of each group's tiles (groups differ in size),
+// the groups one after the other, the largest first.  A tile's first copies are under way before the last
+// tile's sums are stored, and these stores while it is computed.
+// a.splits > 1: the group's rows in so many parts, each part's sums to a.partial.
+template <bool F32>
+__global__ void __launch_bounds__(512, 2) wgrad_kernel(ProductArgs a) {
+  constexpr int BM = 256, BN = 256, BK = 64;
+  typedef ProductTile<false, false, BM, BN, BK, 2, 4, 2, 3> E;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[E::SMEM];
+  const uint32_t per = a.row_tiles * a.col_tiles * a.splits, share = (per + 7) / 8;
+  const uint32_t x = blockIdx.x % 8, step = gridDim.x / 8;
+  // An eighth of a group's tiles, neighbours, is the XCD's; where a group has too few for even eighths, every
+  // eighth of all tiles is.
+  const bool eighths = per >= 64;
+  const uint32_t mine = !eighths ? per : per > x * share ? (per - x * share < share ? per - x * share : share) : 0;
+  const uint64_t items = eighths ? (uint64_t)mine * a.G : ((uint64_t)per * a.G + 7 - x) / 8;
+  GroupTable groups;
+  groups.start(a);
+  struct Item {
+    int64_t count, row0, col0;
+    uint8_t* out;
+  };
   E e;
   e.smem = smem;
-  const int tid = E::thread();
-  e.p.setup(tid, a.P + first * a.L, a.L, row0, a.L - row0);
-  e.q.setup(tid, a.Q + first * a.C, a.C, col0, a.C - col0);
-  if (F32 && a.splits == 1 && a.accumulate && count == 0) return;
-  typename E::Acc acc = {};
-  e.run(count, a.L, a.C, acc);
-  e.template store<F32>(out, a.C, row0, a.L, col0, a.C, F32 && a.splits == 1 && a.accumulate, acc);
+  const auto place = [&](uint64_t i, Item& t) __attribute__((always_inline)) {
+    int64_t g, first;
+    const uint64_t at = eighths ? i : i * 8 + x;
+    groups.nth(a, (int64_t)(at / mine), g, first, t.count);
+    const uint32_t tile = (eighths ? x * share : 0) + (uint32_t)(at % mine), part = tile % a.splits;
+    uint32_t row, col;
+    in_strips(tile / a.splits, a.row_tiles, a.col_tiles, row, col);
+    t.row0 = (int64_t)row * BM;
+    t.col0 = (int64_t)col * BN;
+    t.out = (uint8_t*)a.out + g * a.L * a.C * (F32 ? 4 : 2);
+    if (a.splits > 1) {
+      const int64_t rows = ((t.count + a.splits - 1) / a.splits + BK - 1) / BK * BK;
+      const int64_t from = part * rows < t.count ? part * rows : t.count;
+      first += from;
+      t.count = rows < t.count - from ? rows : t.count - from;
+      t.out = (uint8_t*)(a.partial + (part * a.G + g) * a.L * a.C);
+    }
+    const int tid = E::thread();
+    e.p.setup(tid, a.P + first * a.L, a.L, t.row0, a.L - t.row0);
+    e.q.setup(tid, a.Q + first * a.C, a.C, t.col0, a.C - t.col0);
+    e.template prologue<E::HEAD>(t.count, a.L, a.C);
+  };
+  const bool add = F32 && a.splits == 1 && a.accumulate;
+  // Every second round of the XCD's workgroups is taken from the other end, so that nobody has the larger
+  // groups' tiles in every one.
+  const uint32_t w = blockIdx.x / 8;
+  uint64_t round = 0;
+  const auto item = [&]() { return round * step + (round % 2 ? step - 1 - w : w); };
+  uint64_t i = item();
+  if (i >= items) return;
+  Item t;
+  place(i, t);
+  for (bool stored = false;;) {
+    typename E::Acc acc = {};
+    e.template loop<E::template STORES<F32>>(t.count, a.L, a.C, stored, acc);
+    const Item done = t;
+    ++round;
+    i = item();
+    if (i < items) place(i, t);
+    // (nothing is added to a group without rows)
+    stored = !(add && done.count == 0);
+    if (stored) e.template store_behind<F32>(done.out, a.C, done.row0, a.L, done.col0, a.C, add, acc);
+    if (i >= items) return;
+  }
 }
 
 // The parts' sums added in their order.
@@ -661,17 +782,18 @@ int wgrad_splits(int64_t G, int64_t M, int64_t N, int64_t K) {
   return tiles >= 256 || s < 1 ? 1 : (int)s;
 }
 
-int64_t wgrad_grid(const ProductArgs& a) {
-  return a.G * cdiv(cdiv(a.L, kWgradRows) * cdiv(a.C, kWgradCols) * wgrad_splits(a.G, a.M, a.L, a.C), 8) * 8;
+int64_t wgrad_tiles(const ProductArgs& a) {
+  return cdiv(a.L, kWgradRows) * cdiv(a.C, kWgradCols) * wgrad_splits(a.G, a.M, a.L, a.C);
 }
 
-hipError_t launch_wgrad(bool f32, ProductArgs a, hipStream_t stream) {
+hipError_t launch_wgrad(bool f32, ProductArgs a, int cus, hipStream_t stream) {
   a.row_tiles = cdiv(a.L, kWgradRows);
   a.col_tiles = cdiv(a.C, kWgradCols);
   a.splits = wgrad_splits(a.G, a.M, a.L, a.C);
-  const dim3 grid((uint32_t)wgrad_grid(a));
-  if (f32 || a.splits > 1) hipLaunchKernelGGL((wgrad_kernel<true, 256, 256, 64, 2, 4, 2, 3>), grid, dim3(512), 0, stream, a);
-  else hipLaunchKernelGGL((wgrad_kernel<false, 256, 256, 64, 2, 4, 2, 3>), grid, dim3(512), 0, stream, a);
+  const int64_t tiles = a.G * cdiv(wgrad_tiles(a), 8) * 8, most = cus / 8 > 0 ? cus / 8 * 8 : 8;
+  const dim3 grid((uint32_t)(tiles < most ? tiles : most));
+  if (f32 || a.splits > 1) hipLaunchKernelGGL((wgrad_kernel<true>), grid, dim3(512), 0, stream, a);
+  else hipLaunchKernelGGL((wgrad_kernel<false>), grid, dim3(512), 0, stream, a);
   if (a.splits > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -34,7 +34,7 @@ fp8gg_status check_product(int64_t G, int64_t M, int64_t N, int64_t K) {
   if (N % 8 != 0 || K % 8 != 0)
     return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "N=%lld and K=%lld must be multiples of 8", (long long)N, (long long)K);
   // N and K: the kernels' offsets within 256 rows have 32 bits
-  if (G > kMaxDim || M > kMaxDim || N > (1 << 23) || K > (1 << 23))
+  if (G > kMaxDim || M > kMaxDim || N > (1 << 22) || K > (1 << 22))
     return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "G=%lld total_M=%lld N=%lld K=%lld is too large", (long long)G, (long long)M,
                 (long long)N, (long long)K);
   // tensors of at most 2^47 bytes
@@ -246,8 +246,9 @@ fp8gg_status bf16_grouped_stacked_wgrad(const uint16_t* dY, const uint16_t* X, c
   a.G = G;
   a.partial = static_cast<float*>(workspace);
   a.accumulate = accumulate != 0;
-  FP8GG_TRY(check_grid(wgrad_grid(a)));
-  return launched(launch_wgrad(f32, a, static_cast<hipStream_t>(stream)), "weight gradient");
+  if (wgrad_tiles(a) > 0x7FFFFFFFLL)             // counted in 32 bits
+    return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "N=%lld and K=%lld make too many tiles", (long long)N, (long long)K);
+  return launched(launch_wgrad(f32, a, compute_units(), static_cast<hipStream_t>(stream)), "weight gradient");
 }
 
 fp8gg_status f8f8bf16_quantize_groupwise(const uint16_t* X, uint8_t* XQ, float* x_scale, int64_t rows, int64_t K, void* stream) {

@@ -68,10 +68,10 @@ __host__ __device__ inline int64_t grad_chunks(const void* p, int64_t n, int siz
 int wgrad_splits(int64_t G, int64_t M, int64_t N, int64_t K);
 
 hipError_t launch_product(bool transposed, ProductArgs a, int cus, hipStream_t stream);
-hipError_t launch_wgrad(bool f32, ProductArgs a, hipStream_t stream);
+hipError_t launch_wgrad(bool f32, ProductArgs a, int cus, hipStream_t stream);
 // Workgroups of the largest launch that a product may need, to be checked against the limit.
 int64_t product_grid(const ProductArgs& a);
-int64_t wgrad_grid(const ProductArgs& a);
+int64_t wgrad_tiles(const ProductArgs& a);
 hipError_t launch_quantize_groupwise(const uint16_t* X, uint8_t* XQ, float* x_scale, int64_t rows, int64_t K,
                                      hipStream_t stream);
 hipError_t launch_quantize_weight(const WeightBlocksArgs& a, hipStream_t stream);

@@ -57,7 +57,7 @@ extern "C" {
  * holds, infinities and NaN included, reaches only the results that depend on it.  An empty
  * contraction (K or N = 0) gives zeros.
  *
- * N % 8 == 0, K % 8 == 0, both at most 2^23; tensors 16-byte aligned, M_sizes 8-byte.  G and
+ * N % 8 == 0, K % 8 == 0, both at most 2^22; tensors 16-byte aligned, M_sizes 8-byte.  G and
  * total_M below 2^31 - 256, every tensor at most 2^47 bytes.
  */
 fp8gg_status bf16_grouped_stacked(
