@@ -73,15 +73,17 @@ struct RowTile {
 // most one per group).
 struct RowTiles {
   uint32_t tall, all;
+  uint32_t start, end;           // the first 64 groups' rows, one group per lane
 };
 
 template <int BM>
 __device__ __forceinline__ RowTiles count_row_tiles(const ProductArgs& a) {
   uint32_t rows = 0;
-  RowTiles n = {0, 0};
+  RowTiles n = {0, 0, 0, 0};
   for (int g0 = 0; g0 < a.G; g0 += 64) {
     uint32_t start, end;
     group_rows(a, g0, rows, start, end);
+    if (g0 == 0) n.start = start, n.end = end;
     n.tall += lane_value(wave_scan((end - start + BM / 2 - 1) / BM, AddU{}), 63);
     n.all += lane_value(wave_scan((end - start + BM - 1) / BM, AddU{}), 63);
     rows = lane_value(end, 63);
@@ -95,8 +97,8 @@ __device__ __forceinline__ RowTile find_row_tile(const ProductArgs& a, const Row
   tile -= tall ? 0 : n.tall;
   uint32_t rows = 0, tiles = 0;
   for (int g0 = 0; g0 < a.G; g0 += 64) {
-    uint32_t start, end;
-    group_rows(a, g0, rows, start, end);
+    uint32_t start = n.start, end = n.end;
+    if (g0 > 0) group_rows(a, g0, rows, start, end);
     const uint32_t high = (end - start + BM / 2 - 1) / BM;
     const uint32_t mine = tall ? high : (end - start + BM - 1) / BM - high;
     const uint32_t upto = tiles + wave_scan(mine, AddU{});
@@ -178,7 +180,7 @@ struct Operand {
 
   // The contraction starts at `from`; rows (columns) [first, first + count) of the matrix exist, the
   // tile's other ones repeat the last and their results are dropped.  Offsets stay below 2^32: ld is at
-  // most 2^23, rows of the tile 256.
+  // most 2^22, rows of the tile 256.
   __device__ __forceinline__ void setup(int thread, const uint16_t* from, int64_t ld, int64_t first, int64_t count) {
     tid = thread;
     base = (const uint8_t*)(from + (ALONG ? first * ld : first));
@@ -264,26 +266,36 @@ struct ProductTile {
     else asm volatile("" ::: "memory");
   }
 
+  // Where stage s of nk lies in the contraction of n: from stage `start` on, and round; past the last, n.
+  // start > 0: n % BK == 0.
+  template <bool WHOLE = false>
+  static __device__ __forceinline__ int64_t from(int s, int nk, int start, int64_t n) {
+    if (!WHOLE && s >= nk) return n;
+    const int at = s + start;
+    return (int64_t)(at < nk ? at : at - nk) * BK;
+  }
+
   // Copies of the first stages of a contraction of n: all that the loop starts with, or in two parts, HEAD (all
   // of P's, Q's first) and REST.  No wave reads their slots any more.
   enum Part { ALL, HEAD, REST };
   template <Part PART = ALL>
-  __device__ __forceinline__ void prologue(int64_t n, int64_t ldp, int64_t ldq) const {
+  __device__ __forceinline__ void prologue(int64_t n, int64_t ldp, int64_t ldq, int start = 0) const {
     if (n <= 0) return;
+    const int nk = (int)((n + BK - 1) / BK);
     constexpr int Q0 = PART == REST ? 1 : 0, Q1 = PART == HEAD ? 1 : SQ - 1;
 #pragma unroll
     for (int s = 0; s < (SP > SQ - 1 ? SP : SQ - 1); ++s) {
 #pragma unroll
-      for (int i = 0; PART != REST && s < SP && i < P::LOADS; ++i) p.template issue<false>(i, pslot(s), (int64_t)s * BK, n, ldp);
+      for (int i = 0; PART != REST && s < SP && i < P::LOADS; ++i) p.template issue<false>(i, pslot(s), from(s, nk, start, n), n, ldp);
 #pragma unroll
-      for (int i = 0; s >= Q0 && s < Q1 && i < Q::LOADS; ++i) q.template issue<false>(i, qslot(s), (int64_t)s * BK, n, ldq);
+      for (int i = 0; s >= Q0 && s < Q1 && i < Q::LOADS; ++i) q.template issue<false>(i, qslot(s), from(s, nk, start, n), n, ldq);
     }
   }
 
   // acc += the products over a contraction of n, after its prologue.  YOUNGER: only its HEAD is under way, and
   // behind it, if `younger`, so many stores of each wave, which read from the slots of the REST.
   template <int YOUNGER = 0>
-  __device__ __forceinline__ void loop(int64_t n, int64_t ldp, int64_t ldq, bool younger, Acc& acc) const {
+  __device__ __forceinline__ void loop(int64_t n, int64_t ldp, int64_t ldq, bool younger, Acc& acc, int start = 0) const {
     constexpr bool HEADED = YOUNGER > 0;
     const int wm = wave_id() / WN, wn = wave_id() % WN;
     const int nk = (int)((n + BK - 1) / BK);
@@ -298,7 +310,7 @@ struct ProductTile {
     if (younger) wait_vmcnt_le(FIRST + YOUNGER);
     else wait_vmcnt_le(FIRST);
     barrier();
-    if constexpr (HEADED) prologue<REST>(n, ldp, ldq);
+    if constexpr (HEADED) prologue<REST>(n, ldp, ldq, start);
     v8bf pf[2][FM], qf[2][FN];
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm) pf[0][fm] = p.frag(pslot(0), wm * FM + fm, 0);
@@ -338,11 +350,11 @@ struct ProductTile {
           if (last) {
 #pragma unroll
             for (int r = i * P::LOADS / NM; r < (i + 1) * P::LOADS / NM; ++r)
-              p.template issue<WHOLE>(r, pslot(sp), (int64_t)(kt + SP) * BK, n, ldp);
+              p.template issue<WHOLE>(r, pslot(sp), from<WHOLE>(kt + SP, nk, start, n), n, ldp);
           } else if (ks < QS) {
 #pragma unroll
             for (int r = (ks * NM + i) * Q::LOADS / (QS * NM); r < (ks * NM + i + 1) * Q::LOADS / (QS * NM); ++r)
-              q.template issue<WHOLE>(r, qslot(bq), (int64_t)(kt + SQ - 1) * BK, n, ldq);
+              q.template issue<WHOLE>(r, qslot(bq), from<WHOLE>(kt + SQ - 1, nk, start, n), n, ldq);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -361,9 +373,9 @@ struct ProductTile {
     barrier();
   }
 
-  __device__ __forceinline__ void run(int64_t n, int64_t ldp, int64_t ldq, Acc& acc) const {
-    prologue(n, ldp, ldq);
-    loop(n, ldp, ldq, false, acc);
+  __device__ __forceinline__ void run(int64_t n, int64_t ldp, int64_t ldq, Acc& acc, int start = 0) const {
+    prologue(n, ldp, ldq, start);
+    loop(n, ldp, ldq, false, acc, start);
   }
 
   // Rows [row0, row_end) and columns [col0, cols) of a bf16 output, rounded to nearest even from the fp32
@@ -455,7 +467,7 @@ struct ProductTile {
 // ---------------------------------------------------------------------------
 
 template <typename E, bool Q_ALONG>
-__device__ __forceinline__ void product_tile(const ProductArgs& a, uint8_t* smem, const RowTile& t, int64_t col0) {
+__device__ __forceinline__ void product_tile(const ProductArgs& a, uint8_t* smem, const RowTile& t, int64_t col0, int start = 0) {
   E e;
   e.smem = smem;
   const int tid = E::thread();
@@ -463,54 +475,111 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, uint8_t* smem
   const int64_t ldq = Q_ALONG ? a.L : a.C;
   e.q.setup(tid, a.Q + t.g * a.L * a.C, ldq, col0, a.C - col0);
   typename E::Acc acc = {};
-  e.run(a.L, a.L, ldq, acc);
+  e.run(a.L, a.L, ldq, acc, start);
   e.store((uint16_t*)a.out, a.C, t.row0, t.row_end, col0, a.C, acc);
 }
 
-// One tile per workgroup; workgroups past the last tile end at once.
-template <bool Q_ALONG, int BM, int BN, int BK, int WM, int WN, int SP, int SQ>
-__global__ void __launch_bounds__(WM * WN * 64, 2) product_kernel(ProductArgs a) {
-  typedef ProductTile<true, Q_ALONG, BM, BN, BK, WM, WN, SP, SQ> E;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[E::SMEM];
-  const RowTiles n = count_row_tiles<BM>(a);
-  const uint32_t T = n.all * a.col_tiles;
-  if (blockIdx.x >= T) return;
-  uint32_t row, col;
-  tile_place(n, a.col_tiles, xcd_slot32(blockIdx.x, T), row, col);
-  product_tile<E, Q_ALONG>(a, smem, find_row_tile<BM>(a, n, row), (int64_t)col * BN);
-}
-
-// One workgroup per compute unit; the tiles that do not fill a whole round of them are computed
-// as quarters where two rounds of these take less than a whole tile.
+// One workgroup per compute unit: rounds of whole tiles, and the tiles that do not fill one as halves or
+// quarters where the rounds of these take less.
 template <bool Q_ALONG>
 __global__ void __launch_bounds__(512, 2) product_persistent_kernel(ProductArgs a) {
   constexpr int BM = 256, BN = 256;
   typedef ProductTile<true, Q_ALONG, BM, BN, 64, 2, 4, 2, 3> E;
-  typedef ProductTile<true, Q_ALONG, BM / 2, BN / 2, 64, 2, 4, 5, 5> H;
-  static_assert(H::SMEM <= E::SMEM, "quarters share the ring");
+  typedef ProductTile<true, Q_ALONG, BM / 2, BN, 64, 2, 4, 2, 3> Half;
+  typedef ProductTile<true, Q_ALONG, BM / 2, BN / 2, 64, 2, 4, 5, 5> Quarter;
+  static_assert(Half::SMEM <= E::SMEM && Quarter::SMEM <= E::SMEM, "parts share the ring");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[E::SMEM];
   const uint32_t P = gridDim.x, w = xcd_slot32(blockIdx.x, P);
   const RowTiles n = count_row_tiles<BM>(a);
   const uint32_t T = n.all * a.col_tiles, tall = n.tall * a.col_tiles;
-  // of the last tiles, those with more than half the rows have four quarters, the others two
-  uint32_t whole = T / P * P;
-  const uint32_t four = tall > whole ? tall - whole : 0, two = T - whole - four;
-  const uint32_t quarters = 4 * four + 2 * two;
-  if (quarters > 2 * P) whole = T;
+  // Rounds of whole tiles: as many as the tall ones fill, as all fill, or all.  Of the tiles behind them the tall
+  // ones have two halves, the others one.  A round of halves takes 0.6 of one of whole tiles, of quarters 0.4
+  // (4096 rows in one group, N = 2048, K = 4096, whose 128 tiles fill half a round: 96 us whole, 58 as halves,
+  // 73 as two rounds of quarters).
+  uint32_t whole = T, rest = 0, halves = 0, parts = 1, least = (T + P - 1) / P * 10;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t full = (c ? T : tall) / P, at = full * P, r = tall > at ? tall - at : 0, h = T - at + r;
+    const uint32_t by_half = (h + P - 1) / P * 6, by_quarter = (2 * h + P - 1) / P * 4;
+    const uint32_t cost = full * 10 + (by_half < by_quarter ? by_half : by_quarter);
+    if (cost < least) least = cost, whole = at, rest = r, halves = h, parts = by_quarter < by_half ? 2 : 1;
+  }
   uint32_t row, col;
   for (uint32_t tile = w; tile < whole; tile += P) {
     tile_place(n, a.col_tiles, tile, row, col);
     product_tile<E, Q_ALONG>(a, smem, find_row_tile<BM>(a, n, row), (int64_t)col * BN);
   }
-  if (whole == T) return;
-  for (uint32_t i = w; i < quarters; i += P) {
-    const bool tallest = i < 4 * four;
-    const uint32_t at = tallest ? i : i - 4 * four, part = tallest ? at % 4 : at % 2;
-    tile_place(n, a.col_tiles, whole + (tallest ? at / 4 : four + at / 2), row, col);
+  for (uint32_t i = w; i < halves * parts; i += P) {
+    const uint32_t half = i / parts;
+    const bool in_tall = half < 2 * rest;
+    tile_place(n, a.col_tiles, whole + (in_tall ? half / 2 : half - rest), row, col);
     RowTile t = find_row_tile<BM>(a, n, row);
-    t.row0 += part / 2 * (BM / 2);
-    const int64_t col0 = (int64_t)col * BN + part % 2 * (BN / 2);
-    if (t.row0 < t.row_end && col0 < a.C) product_tile<H, Q_ALONG>(a, smem, t, col0);
+    t.row0 += in_tall ? half % 2 * (BM / 2) : 0;
+    const int64_t col0 = (int64_t)col * BN + i % parts * (BN / 2);
+    if (parts == 1) product_tile<Half, Q_ALONG>(a, smem, t, col0);
+    else if (col0 < a.C) product_tile<Quarter, Q_ALONG>(a, smem, t, col0);
+  }
+}
+
+// The same with tiles of half the rows, for groups whose weights' way from memory is the bound: a tile's first
+// copies are under way before the last tile's output is stored, and these stores while it is computed.  Forward, groups start at
+// different places of the contraction: rows that lie a power of two apart and are read at the same place keep
+// only some of the memory's channels busy (256 rows in 32 groups, N = K = 2048: 61 -> 45 us; 1536 rows in 16,
+// N = K = 4096: 145 -> 131).  Different places for a group's own tiles gain less, as these share the rows of
+// its input (47, 146), and the input's gradient, whose reads run along the rows of W, nothing.
+template <bool Q_ALONG>
+__global__ void __launch_bounds__(512, 2) product_stream_kernel(ProductArgs a) {
+  constexpr int BM = 128, BN = 256, BK = 64;
+  typedef ProductTile<true, Q_ALONG, BM, BN, BK, 2, 4, 2, 3> E;
+  typedef ProductTile<true, Q_ALONG, BM, BN / 2, BK, 2, 4, 5, 5> H;
+  static_assert(H::SMEM >= E::SMEM, "both share the ring");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[H::SMEM];
+  const uint32_t P = gridDim.x, w = xcd_slot32(blockIdx.x, P);
+  const RowTiles n = count_row_tiles<BM>(a);
+  const uint32_t T = n.all * a.col_tiles;
+  uint32_t whole = T / P * P;
+  if (2 * (T - whole) > P) whole = T;
+  const int64_t ldq = Q_ALONG ? a.L : a.C;
+  struct Item {
+    RowTile rows;
+    int64_t col0;
+    int start;
+  };
+  const auto find = [&](uint32_t tile, Item& t) __attribute__((always_inline)) {
+    uint32_t row, col;
+    tile_place(n, a.col_tiles, tile, row, col);
+    t.rows = find_row_tile<BM>(a, n, row);
+    t.col0 = (int64_t)col * BN;
+    t.start = Q_ALONG && a.L > 0 && a.L % BK == 0 ? (uint32_t)t.rows.g * 5u % (uint32_t)(a.L / BK) : 0;
+  };
+  E e;
+  e.smem = smem;
+  const auto place = [&](uint32_t tile, Item& t) __attribute__((always_inline)) {
+    find(tile, t);
+    const int tid = E::thread();
+    e.p.setup(tid, a.P, a.L, t.rows.row0, t.rows.row_end - t.rows.row0);
+    e.q.setup(tid, a.Q + t.rows.g * a.L * a.C, ldq, t.col0, a.C - t.col0);
+    e.template prologue<E::HEAD>(a.L, a.L, ldq, t.start);
+  };
+  Item t;
+  uint32_t tile = w;
+  if (tile < whole) {
+    place(tile, t);
+    for (bool stored = false;; stored = true) {
+      typename E::Acc acc = {};
+      e.template loop<E::template STORES<false>>(a.L, a.L, ldq, stored, acc, t.start);
+      const Item done = t;
+      tile += P;
+      if (tile < whole) place(tile, t);
+      e.template store_behind<false>(a.out, a.C, done.rows.row0, done.rows.row_end, done.col0, a.C, false, acc);
+      if (tile >= whole) break;
+    }
+    E::barrier();
+  }
+  for (uint32_t i = w; i < 2 * (T - whole); i += P) {
+    find(whole + i / 2, t);
+    const int64_t col0 = t.col0 + i % 2 * (BN / 2);
+    if (col0 < a.C) product_tile<H, Q_ALONG>(a, smem, t.rows, col0, t.start);
   }
 }
 
@@ -719,14 +788,19 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Row tiles of the grouped output, whatever the groups' sizes.
 int64_t most_row_tiles(const ProductArgs& a, int64_t BM) { return a.M / BM + (a.G < a.M ? a.G : a.M); }
 
-enum Variant { kSplit, kRows32, kRows128, kPersistent };
+enum Variant { kSplit, kStream, kPersistent };
 
+// Few tiles of 32 x 128 leave compute units idle unless the contraction is split (8 to 256 such tiles, us split
+// and by tiles of 128 x 256: one row of 4096 x 7168, 13 / 49 forward, 16 / 31 input's gradient; 128 rows in 2
+// groups, N = 2048, K = 4096, 18 / 32 and 20 / 19; 24 rows in 4, N = 4096, K = 2048, 16 / 22 and 17 / 33; 16 in 8,
+// N = 4096, K = 7168, 60 / 66 forward).  Groups of few rows are bound by the weights' way from memory, which tiles
+// of 128 rows with their stores behind the next tile keep busiest; large ones by the matrix units, which tiles of
+// 256 x 256 feed with half the reads (us at 128 / 256 rows: 8 groups of 512, N = 4096, K = 7168, 288 / 254;
+// 8 of 350, N = 4096, K = 2048, 75 / 62 for the input's gradient; 8 of 187, N = K = 4096, 76 / 76; 16 of 156,
+// N = K = 2048, 41 / 43).
 Variant variant_of(const ProductArgs& a) {
   if (most_row_tiles(a, 32) * cdiv(a.C, 128) <= 256) return kSplit;
-  const int64_t rows = a.M / a.G;
-  if (rows < 24) return kRows32;
-  if (rows < 192) return kRows128;
-  return kPersistent;
+  return a.M / a.G < 192 ? kStream : kPersistent;
 }
 
 template <bool Q_ALONG>
@@ -740,15 +814,9 @@ hipError_t launch_rows(ProductArgs a, int cus, hipStream_t stream) {
       else hipLaunchKernelGGL((product_split_kernel<false, 64, 64, 4, 3>), grid, dim3(256), 0, stream, a);
       break;
     }
-    case kRows32:
-      a.col_tiles = cdiv(a.C, 128);
-      hipLaunchKernelGGL((product_kernel<Q_ALONG, 32, 128, 64, 1, 4, 4, 4>), dim3((uint32_t)(most_row_tiles(a, 32) * a.col_tiles)),
-                         dim3(256), 0, stream, a);
-      break;
-    case kRows128:
-      a.col_tiles = cdiv(a.C, 128);
-      hipLaunchKernelGGL((product_kernel<Q_ALONG, 128, 128, 64, 2, 2, 2, 3>),
-                         dim3((uint32_t)(most_row_tiles(a, 128) * a.col_tiles)), dim3(256), 0, stream, a);
+    case kStream:
+      a.col_tiles = cdiv(a.C, 256);
+      hipLaunchKernelGGL((product_stream_kernel<Q_ALONG>), dim3((uint32_t)cus), dim3(512), 0, stream, a);
       break;
     case kPersistent:
       a.col_tiles = cdiv(a.C, 256);
@@ -761,11 +829,8 @@ hipError_t launch_rows(ProductArgs a, int cus, hipStream_t stream) {
 }  // namespace
 
 int64_t product_grid(const ProductArgs& a) {
-  switch (variant_of(a)) {
-    case kRows32: return most_row_tiles(a, 32) * cdiv(a.C, 128);
-    case kRows128: return most_row_tiles(a, 128) * cdiv(a.C, 128);
-    default: return most_row_tiles(a, 256) * cdiv(a.C, 256);    // tiles, which are counted in 32 bits
-  }
+  // tiles, which are counted in 32 bits
+  return variant_of(a) == kStream ? most_row_tiles(a, 128) * cdiv(a.C, 256) : most_row_tiles(a, 256) * cdiv(a.C, 256);
 }
 
 hipError_t launch_product(bool transposed, ProductArgs a, int cus, hipStream_t stream) {

@@ -99,6 +99,27 @@ def test_products(F, G, M, N, K, how):
     check(out, want + held.double(), size + held.double().abs(), M, False, "wgrad accumulated")
 
 
+# tiles over several rounds of the compute units, the last of them whole, in halves or in quarters, for small
+# and large groups, and contractions that groups start at different places
+@pytest.mark.parametrize("G,M,N,K", [
+    (24, 1500, 2056, 256), (20, 600, 4104, 192), (67, 3000, 1280, 1024), (9, 1000, 2056, 64), (33, 700, 640, 4104),
+    (1, 4096, 2056, 128), (1, 1024, 2048, 64), (3, 6000, 2312, 128), (2, 5000, 264, 2568), (5, 3000, 192, 4360)])
+@pytest.mark.parametrize("how", ["even", "skewed", "short"])
+def test_products_in_rounds(F, G, M, N, K, how):
+    print(f"case rounds G={G} M={M} N={N} K={K} {how}", flush=True)
+    x, w, dy = inputs(G, M, N, K, seed=3)
+    s = sizes_of(G, M, how)
+    for name, call, args, width, L, oracle in (("forward", F.bf16_grouped_stacked, (x, w), N, K, O.forward),
+                                               ("dgrad", F.bf16_grouped_stacked_dgrad, (dy, w), K, N, O.dgrad)):
+        out = P.Guarded((M, width), torch.bfloat16)
+        call(*args, dev(s), **{"Y" if name == "forward" else "dX": out.t})
+        torch.cuda.synchronize()
+        out.check(name)
+        want, size, written = oracle(args[0].double(), args[1].double(), s)
+        check(out.t[written], want[written], size[written], L, True, name)
+        assert out.untouched((~written).numpy()).all(), f"{name}: a row past the groups' end was written"
+
+
 @pytest.mark.parametrize("G,M,N,K", [(1, 12000, 128, 72), (2, 5003, 264, 136), (3, 40000, 8, 8)])
 def test_wgrad_in_parts(F, G, M, N, K):
     """Few tiles and many rows: the rows are split, also where a group has fewer than the others' parts."""
