@@ -11,9 +11,14 @@ Backward:  from the gradient of the layer's output to those of its input, of the
            keeps of the activations is in 8 bits: the fp8 rows that the products read and
            the checkpoint of the gated activation's input.
 
+Training:  ``train_step`` keeps fp32 weights, quantises them for the block-scaled products
+           of both passes (or uses bf16 products instead), adds the weights' gradients up in
+           fp32 over micro-batches with bf16 products, clips them by their common norm, and
+           updates the weights.
+
 The router's own product (tokens x hidden x experts, small) is torch's.  ``main`` runs the
 layer on random data, compares it with the same layer in fp32 torch operations, and
-times both passes.
+times both passes and a training step.
 """
 from __future__ import annotations
 
@@ -100,6 +105,76 @@ def backward(dout, dresidual, w: Weights, q: dict, kept):
     return dx, dnorm_w, drouter, dw1, dw2
 
 
+def train_operands(w: Weights, fp8: bool) -> dict:
+    """The products' operands of one step, from the fp32 weights: codes with a scale per 128 x 128
+    values, as they are and transposed, or bf16, whose products read one layout in both passes."""
+    if fp8:
+        return {n: F.f8f8bf16_quantize_groupwise_weight(getattr(w, n), transposed=True) for n in ("w1", "w2")}
+    return {n: getattr(w, n).to(torch.bfloat16) for n in ("w1", "w2")}
+
+
+def train_product(rows, rows_bf16, q, M_sizes):
+    """rows (codes and scales, which fp8 products read) or the same in bf16, times an expert weight."""
+    if isinstance(q, F.WeightBlocks):
+        return F.f8f8bf16_groupwise_grouped_stacked(rows[0], q.WQ, rows[1], q.w_scale, M_sizes)
+    return F.bf16_grouped_stacked(rows_bf16, q, M_sizes)
+
+
+def train_dgrad(dy, q, M_sizes):
+    """The gradient of train_product's rows."""
+    if isinstance(q, F.WeightBlocks):
+        dyq, dys = F.f8f8bf16_quantize_groupwise(dy)
+        return F.f8f8bf16_groupwise_grouped_stacked(dyq, q.WQt, dys, q.wt_scale, M_sizes)
+    return F.bf16_grouped_stacked_dgrad(dy, q, M_sizes)
+
+
+def train_forward(x, residual, w: Weights, q: dict, k: int):
+    """forward with the operands of train_operands: hidden and inner sizes that are multiples of 128."""
+    norm = F.f8f8bf16_rmsnorm_quantize(x, w.norm, residual=residual, block=128, want_y=True, want_rstd=True)
+    logits = norm.Y.float() @ w.router.t()
+    route = F.f8f8bf16_route(logits, k, bias=w.bias, score="sigmoid")
+    rows = F.f8f8bf16_moe_dispatch(norm.XQ, norm.x_scale, route.dst_row)
+    xb, _ = F.f8f8bf16_moe_combine_backward(norm.Y, route.dst_row)       # the same rows in bf16
+    h = train_product(rows, xb, q["w1"], route.M_sizes)
+    act = F.f8f8bf16_silu_mul_quantize(h, block=128, checkpoint=True)
+    ab = (act.AQ.view(torch.float8_e4m3fn).float().unflatten(1, (-1, 128)) * act.a_scale[:, :, None]).flatten(1).to(torch.bfloat16)
+    y = train_product(act, ab, q["w2"], route.M_sizes)
+    out = F.f8f8bf16_moe_combine(y, route.dst_row, route.weights)
+    return out, norm.residual, (norm, logits, route, xb, act, ab, y)
+
+
+def train_backward(dout, dresidual, w: Weights, q: dict, kept, grads: dict):
+    """Adds the weights' gradients to `grads` (fp32) and returns that of input and residual."""
+    norm, logits, route, xb, act, ab, y = kept
+    M = route.M_sizes
+    dy, dweights = F.f8f8bf16_moe_combine_backward(dout, route.dst_row, route.weights, y)
+    da = train_dgrad(dy, q["w2"], M)
+    F.bf16_grouped_stacked_wgrad(dy, ab, M, dW=grads["w2"], accumulate=True)
+    dh = F.f8f8bf16_silu_mul_backward(da, act.HQ, act.h_scale)
+    drows = train_dgrad(dh, q["w1"], M)
+    F.bf16_grouped_stacked_wgrad(dh, xb, M, dW=grads["w1"], accumulate=True)
+    dlogits = F.f8f8bf16_route_backward(logits, route.ids, dweights, score="sigmoid")
+    grads["router"] += dlogits.t() @ norm.Y.float()
+    dnorm = F.f8f8bf16_moe_combine(drows, route.dst_row, addend=(dlogits @ w.router).to(torch.bfloat16))
+    dx, dnorm_w = F.f8f8bf16_rmsnorm_backward(dnorm, norm.residual, w.norm, norm.rstd, dresidual=dresidual)
+    grads["norm"] += dnorm_w
+    return dx
+
+
+def train_step(batches, w: Weights, k: int, lr: float = 1e-3, max_norm: float = 1.0, fp8: bool = True):
+    """One step of plain gradient descent over micro-batches, each (x, residual, gradients of the layer's two
+    outputs), with the gradients clipped by their common norm.  Returns (the clipped gradients, norm)."""
+    q = train_operands(w, fp8)
+    grads = {n: torch.zeros_like(getattr(w, n)) for n in ("norm", "router", "w1", "w2")}
+    for x, residual, dout, dresidual in batches:
+        _, _, kept = train_forward(x, residual, w, q, k)
+        train_backward(dout, dresidual, w, q, kept, grads)
+    norm = F.f8f8bf16_grad_clip(list(grads.values()), max_norm)
+    for n, g in grads.items():
+        getattr(w, n).sub_(g, alpha=lr)
+    return grads, norm
+
+
 def reference(x, residual, w: Weights, ids, dout, dresidual):
     """The same layer in fp32, the choice of experts given: (output, gradients)."""
     h = (x.float() + residual.float()).to(torch.bfloat16).float().requires_grad_(True)
@@ -148,6 +223,11 @@ def main() -> None:
         return (time.perf_counter() - t) / a.steps * 1e6
     print(f"forward  {timed(lambda: forward(x, residual, w, q, a.topk)):9.1f} us")
     print(f"backward {timed(lambda: backward(dout, dres, w, q, kept)):9.1f} us")
+    if a.hidden % 128 == 0 and a.inner % 128 == 0:
+        batch = [(x, residual, dout, dres)]
+        for fp8 in (True, False):
+            us = timed(lambda: train_step(batch, w, a.topk, fp8=fp8))
+            print(f"training step, {'fp8' if fp8 else 'bf16'} products {us:9.1f} us")
 
 
 if __name__ == "__main__":
