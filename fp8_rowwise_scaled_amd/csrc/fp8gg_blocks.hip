@@ -10,6 +10,28 @@ namespace fp8gg {
 
 namespace {
 
+// 448 / amax in two parts, whose sum has twice fp32's bits: a value's quotient by its scale is then rounded once
+// before its code is, and bf16 values, whose quotients are the middle between two codes or well away from it, get
+// the nearest code, ties the even one.  fp32 values need the rest that this rounding drops: where it leaves the
+// middle, `nearest` goes a step to the rest's side.  (v times the rounded inverse puts one value in 10^6 on the
+// wrong side; the times are the same.)  The second part is 0 where amax is not finite.
+struct Inverse {
+  float hi, lo;
+  __device__ __forceinline__ explicit Inverse(float amax) {
+    const float a = floored(amax);
+    hi = inverse_scale(amax);
+    lo = mag(amax) < 0x7F800000u ? __builtin_fmaf(-hi, a, kCodeMax) / a : 0.f;
+  }
+  __device__ __forceinline__ float operator()(float v) const { return __builtin_fmaf(v, hi, v * lo); }
+  __device__ __forceinline__ float nearest(float v) const {
+    const float low = v * lo, q = __builtin_fmaf(v, hi, low), rest = __builtin_fmaf(v, hi, -q) + low;
+    const uint32_t u = __float_as_uint(q);
+    // the middle between two codes has 19 zeros at its end; a step from any other such number keeps its code
+    const bool even = (u & 0xFFFFu) == 0 && rest != 0.f && mag(q) - 1u < 0x7F7FFFFFu;
+    return even ? __uint_as_float((rest > 0.f) == (q > 0.f) ? u + 1 : u - 1) : q;
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Rows
 // ---------------------------------------------------------------------------
@@ -27,13 +49,16 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_groupwise_kernel(const 
                                                                           float* __restrict__ x_scale, int64_t parts) {
   // part: sixteen values, an eighth of a block
   for (int64_t i = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x; i < parts; i += (int64_t)gridDim.x * kRowsThreads) {
-    const F8 lo = unpack_bf16(load_in<STREAM>(X + 2 * i)), hi = unpack_bf16(load_in<STREAM>(X + 2 * i + 1));
+    F8 lo = unpack_bf16(load_in<STREAM>(X + 2 * i)), hi = unpack_bf16(load_in<STREAM>(X + 2 * i + 1));
     uint32_t m = mag_max(hi, mag_max(lo, 0));
     m = umax(m, dpp<0xB1>(m));     // lanes 1 0 3 2
     m = umax(m, dpp<0x4E>(m));     // lanes 2 3 0 1
     m = umax(m, dpp<0x141>(m));    // mirror in each half row of eight
-    const float amax = __uint_as_float(m), inv = inverse_scale(amax);
-    const u32x2 a = codes_of(lo, inv), b = codes_of(hi, inv);
+    const float amax = __uint_as_float(m);
+    const Inverse inv(amax);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) lo.v[e] = inv(lo.v[e]), hi.v[e] = inv(hi.v[e]);
+    const u32x2 a = codes_of(lo, 1.f), b = codes_of(hi, 1.f);
     store_out(XQ + i, u32x4{a[0], a[1], b[0], b[1]});
     if (i % 8 == 0) x_scale[i / 8] = scale_of(amax);
   }
@@ -54,9 +79,13 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_groupwise_kernel(const 
 
 constexpr int kWeightThreads = 256;
 
-__device__ __forceinline__ uint32_t codes4(const f32x4& v, float inv) {
-  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true);
+template <bool F32>
+__device__ __forceinline__ uint32_t codes4(const f32x4& v, const Inverse& inv) {
+  float x[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = F32 ? inv.nearest(v[e]) : inv(v[e]);
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true);
 }
 
 template <bool F32, bool T>
@@ -88,11 +117,12 @@ __global__ void __launch_bounds__(kWeightThreads) quantize_weight_kernel(WeightB
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWeightThreads / 64; ++w) m = umax(m, wave_max[w]);
-  const float amax = __uint_as_float(m), inv = inverse_scale(amax);
+  const float amax = __uint_as_float(m);
+  const Inverse inv(amax);
   uint32_t q[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    q[i] = codes4(v[i], inv);
+    q[i] = codes4<F32>(v[i], inv);
     store_out((uint32_t*)(a.WQ + first + i * a.K), q[i]);
   }
   const int64_t g = gy / nb, y = gy % nb;
