@@ -170,8 +170,10 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(GradArgs a, const 
   __shared__ double lds[kThreads / 64];
   const double norm = __builtin_sqrt(join(partial, n, lds));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  const double factor = max_norm / (norm + eps);
-  const bool keep = factor >= 1.0;               // false for NaN, which reaches the gradients
+  // Without a bound, or over a denominator of 0, there is nothing to scale down, whatever the norm: the quotient would be
+  // NaN there.  Otherwise only a NaN norm gives NaN, which reaches the gradients (the comparison is false).
+  const double under = norm + eps, factor = __builtin_isinf(max_norm) || under == 0.0 ? 1.0 : max_norm / under;
+  const bool keep = factor >= 1.0;
   const float f = keep ? 1.0f : (float)factor;
   const Firsts first(a);
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {

@@ -67,7 +67,8 @@ def f8f8bf16_grad_square_sum(grads, square_sum=None, workspace=None):
 
 def f8f8bf16_grad_clip(grads, max_norm, eps=1e-6, square_sum=None, outs=None, norm=None, workspace=None):
     """Scales a list of float32 or bf16 gradients by min(1, max_norm / (norm + eps)), in
-    place or into the tensors of outs (of the same shapes, types and strides).  norm is the
+    place or into the tensors of outs (of the same shapes, types and strides).  An infinite
+    max_norm leaves every value as it is, whatever the norm.  norm is the
     square root of square_sum (float64 [1], as grad_square_sum gives it) or, if that is None,
     of the gradients' own.  Returns norm, float32 [1], on the device."""
     return _binding().grad_clip(grads, max_norm, eps, square_sum, outs, norm, workspace)

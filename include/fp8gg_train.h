@@ -106,7 +106,8 @@ fp8gg_status f8f8bf16_quantize_groupwise_weight(
  *
  *     square_sum = sum_i sum_j grads[i][j]^2                       (fp64)
  *     norm       = sqrt(square_sum)
- *     outs[i]    = grads[i] * min(1, max_norm / (norm + eps))      (rounded to the type)
+ *     outs[i]    = grads[i] * factor                               (rounded to the type)
+ *     factor     = min(1, max_norm / (norm + eps));  1 where max_norm is infinite or norm + eps is 0
  *
  *   grads, outs   n device pointers each, in host memory: bf16 or fp32 tensors (dtypes),
  *                 counts[i] values, aligned to their type; an empty tensor's may be NULL.
@@ -115,13 +116,14 @@ fp8gg_status f8f8bf16_quantize_groupwise_weight(
  *   square_sum    [1] fp64: grad_square_sum writes it; grad_clip takes it where it is given
  *                 (sums of several ranks, added up), else (NULL) forms its own
  *   norm          [1] fp32 (infinite where fp32 does not hold it; the factor goes by fp64's)
- *   max_norm      >= 0, infinity: the norm alone            eps  >= 0
+ *   max_norm      >= 0, infinity: the norm alone            eps  >= 0, finite
  *   workspace     f8f8bf16_grad_workspace(n) bytes, 16-byte aligned; not read where
  *                 grad_clip is given square_sum
  *
- * A norm that is infinite gives the factor 0 (finite gradients become 0, infinite ones
- * NaN), one that is NaN makes every gradient NaN.  The factor is rounded to fp32 before it
- * multiplies.
+ * Under a finite max_norm a norm that is infinite gives the factor 0 (finite gradients become
+ * 0, infinite ones NaN), one that is NaN makes every gradient NaN.  Under an infinite max_norm
+ * the factor is 1 whatever the norm, so that a step can be left out by its norm.  The factor
+ * is rounded to fp32 before it multiplies.
  */
 fp8gg_status f8f8bf16_grad_square_sum(
     const void* const* grads, const int64_t* counts, const int32_t* dtypes, int64_t n, double* square_sum,

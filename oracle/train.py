@@ -78,5 +78,8 @@ def weight_blocks(w):
 def clip(grads, max_norm, eps):
     """(norm, factor, scaled gradients)."""
     norm = math.sqrt(math.fsum(float(v) for g in grads for v in g.double().flatten().square().split(1 << 16) for v in [v.sum()]))
-    factor = min(1.0, max_norm / (norm + eps))
+    if math.isinf(max_norm) or norm + eps == 0:
+        factor = 1.0
+    else:
+        factor = math.nan if math.isnan(norm) else min(1.0, max_norm / (norm + eps))
     return norm, factor, [g.double() * factor for g in grads]

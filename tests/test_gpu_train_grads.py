@@ -102,6 +102,33 @@ def test_infinite_and_nan_gradients(F):
     assert math.isnan(float(F.f8f8bf16_grad_clip(a, 1.0))) and all(bool(g.isnan().all()) for g in a)
 
 
+@pytest.mark.parametrize("into", [False, True])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_an_infinite_bound_leaves_every_gradient(F, bad, into):
+    """The norm alone: also where it is infinite or NaN, no value changes, in place or on its way into outs."""
+    g = make([5000, 3000, 20000])
+    g[0][17] = bad
+    before = [t.clone() for t in g]
+    outs = [torch.full_like(t, 7.0) for t in g] if into else None
+    norm = float(F.f8f8bf16_grad_clip(g, float("inf"), outs=outs))
+    assert math.isnan(norm) if math.isnan(bad) else norm == math.inf
+    for a, b in zip(outs if into else g, before):
+        keep = ~b.isnan()
+        assert torch.equal(a[keep], b[keep]) and bool(a[~keep].isnan().all())
+    assert float(F.f8f8bf16_grad_clip(g, float("inf"), square_sum=torch.full((1,), math.inf, dtype=torch.float64, device="cuda"))) == math.inf
+    assert torch.equal(g[1], before[1]) and torch.equal(g[2], before[2])
+
+
+@pytest.mark.parametrize("into", [False, True])
+def test_zeros_stay_zeros_without_eps(F, into):
+    """The factor's denominator is 0 there: nothing to scale down, whatever the bound."""
+    for bound in (0.0, 1.0, float("inf")):
+        g = [torch.zeros(5000, device="cuda"), torch.zeros(3000, dtype=torch.bfloat16, device="cuda")]
+        outs = [torch.full_like(t, 7.0) for t in g] if into else None
+        assert float(F.f8f8bf16_grad_clip(g, bound, eps=0.0, outs=outs)) == 0.0
+        assert not any(bool((t != 0).any()) for t in (outs or g))
+
+
 @pytest.mark.parametrize("offset", range(8))
 def test_views_at_any_alignment(F, offset):
     """Tensors one after another in a flat buffer, in place and into a buffer aligned otherwise; what lies around them stays."""

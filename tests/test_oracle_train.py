@@ -72,3 +72,16 @@ def test_clip():
     norm, factor, out = O.clip([a, b], 1.0, 0.0)
     assert norm == 5.0 and factor == 0.2 and [o.tolist() for o in out] == [[0.6000000000000001], [[0.0, 0.8]]]
     assert O.clip([a, b], 10.0, 0.0)[1] == 1.0 and O.clip([a, b], 1.0, 5.0)[1] == 0.1 and O.clip([], 1.0, 1e-6)[0] == 0.0
+
+
+def test_clip_where_the_quotient_is_none():
+    """An infinite bound and a norm of 0 without eps leave every value; an infinite norm under a bound gives 0, a NaN one NaN."""
+    inf, nan = math.inf, math.nan
+    for bad in (inf, -inf, nan):
+        _, factor, out = O.clip([torch.tensor([1.0, bad])], inf, 0.0)
+        assert factor == 1.0 and out[0][0] == 1.0
+    assert O.clip([torch.zeros(3)], 0.0, 0.0)[1] == 1.0
+    assert not O.clip([torch.zeros(3)], 0.0, 0.0)[2][0].any()
+    _, factor, out = O.clip([torch.tensor([1.0, inf])], 2.0, 0.0)
+    assert factor == 0.0 and out[0][0] == 0.0 and out[0][1].isnan()
+    assert math.isnan(O.clip([torch.tensor([1.0, nan])], 2.0, 0.0)[1])
