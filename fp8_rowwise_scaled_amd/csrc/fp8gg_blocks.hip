@@ -13,8 +13,12 @@ namespace {
 // 448 / amax in two parts, whose sum has twice fp32's bits: a value's quotient by its scale is then rounded once
 // before its code is, and bf16 values, whose quotients are the middle between two codes or well away from it, get
 // the nearest code, ties the even one.  fp32 values need the rest that this rounding drops: where it leaves the
-// middle, `nearest` goes a step to the rest's side.  (v times the rounded inverse puts one value in 10^6 on the
-// wrong side; the times are the same.)  The second part is 0 where amax is not finite.
+// middle, `nearest` goes a step to the rest's side.  A quotient that is not the middle m itself (5 bits) is 2^-28.95 of m
+// away at least: 448 |v| and m amax are whole numbers of some unit below 31 * 2^24.  One that is has a rest of rounding
+// errors alone, below 2^-31 of m: those of the second part, which is off by 2^-24 of itself or, below fp32's normal range
+// (amax above 2^109), by 2^-150, that is 2^-31.8 of the first part at the largest amax.  So 2^-30 tells the two apart.
+// (v times the rounded inverse puts one value in 10^6 on the wrong side; the times are the same.)  The second part is 0
+// where amax is not finite.
 struct Inverse {
   float hi, lo;
   __device__ __forceinline__ explicit Inverse(float amax) {
@@ -27,8 +31,8 @@ struct Inverse {
     const float low = v * lo, q = __builtin_fmaf(v, hi, low), rest = __builtin_fmaf(v, hi, -q) + low;
     const uint32_t u = __float_as_uint(q);
     // the middle between two codes has 19 zeros at its end; a step from any other such number keeps its code
-    const bool even = (u & 0xFFFFu) == 0 && rest != 0.f && mag(q) - 1u < 0x7F7FFFFFu;
-    return even ? __uint_as_float((rest > 0.f) == (q > 0.f) ? u + 1 : u - 1) : q;
+    const bool off = (u & 0xFFFFu) == 0 && __builtin_fabsf(rest) > 0x1p-30f * __builtin_fabsf(q);
+    return off ? __uint_as_float((rest > 0.f) == (q > 0.f) ? u + 1 : u - 1) : q;
   }
 };
 

@@ -73,7 +73,9 @@ int64_t bf16_grouped_stacked_wgrad_workspace(int64_t G, int64_t total_M, int64_t
 
 /*
  * Rows as an operand of the block-scaled products: one scale per row and 128 columns.  Codes
- * and scales are those of fp8gg_layer.h (s = max(amax, 2^-100) / 448, 1 when amax is 0).
+ * and scales are those of fp8gg_layer.h (s = max(amax, 2^-100) / 448, 1 when amax is 0), but
+ * for the midpoints: here a code is always the nearest to the value over the real s (of
+ * which the scale returned is a rounding), ties to the even one.  The same of the weights' below.
  *
  *   X        [rows, K]         bf16
  *   XQ       [rows, K]         e4m3fn

@@ -13,6 +13,8 @@ import torch
 from .layer import E4M3_MAX
 
 BLOCK = 128
+# Of codes 0 to 126: eight subnormal ones, then eight to a power of two.
+E4M3_MAGNITUDES = [(i % 8 + 8 * (i > 7)) * 2.0 ** (max(i // 8, 1) - 10) for i in range(127)]
 
 
 def group_rows(sizes, M: int) -> list[range]:
@@ -73,6 +75,20 @@ def weight_blocks(w):
     b = w.view(G, N // BLOCK, BLOCK, K // BLOCK, BLOCK)
     s = scale_of(b.abs().amax(4).amax(2))
     return (b / s[:, :, None, :, None]).view(G, N, K), s
+
+
+def nearest(codes, v, amax):
+    """Which e4m3 codes (uint8) are the nearest to v / s, s = max(amax, 2^-100) / 448, ties to the even one.  v and amax hold
+    fp32 values: 448 |v| and a middle of two codes (5 bits) times amax have less than 53 bits, so both are exact here."""
+    table = torch.tensor([E4M3_MAGNITUDES[i] for i in range(127)], dtype=torch.float64, device=v.device)
+    i = (codes & 0x7F).long()
+    amax = amax.clamp_min(2.0 ** -100)
+    x, even = v.abs() * E4M3_MAX, i % 2 == 0
+    here = table[i.clamp_max(126)]
+    low = (here + table[(i - 1).clamp(0, 126)]) / 2 * amax
+    high = torch.where(i < 126, (here + table[(i + 1).clamp_max(126)]) / 2 * amax, math.inf)
+    sign = (codes >= 0x80) == (v < 0)
+    return (i < 127) & ((x > low) | (x == low) & even | (i == 0)) & ((x < high) | (x == high) & even) & (sign | (i == 0))
 
 
 def clip(grads, max_norm, eps):

@@ -49,6 +49,57 @@ def test_rows(F, rows, K):
     P.assert_codes(q.t, want.cpu().numpy(), REL, "codes")
 
 
+def bf16_blocks():
+    """Blocks [n, 128] that hold every 8-bit significand under every 8-bit largest value, at 14 distances below it and at
+    magnitudes from where the scale's floor acts up to the type's largest: whatever ties there are, and their neighbours."""
+    blocks = []
+    for top in (-112, -99, -60, 0, 40, 127):
+        for below in range(1, 15):
+            amax = torch.arange(128, 256, device="cuda").double() * 2.0 ** (top - 7)
+            b = (torch.arange(128, 256, device="cuda").double() * 2.0 ** (top - below - 7)).repeat(128, 1)
+            b[:, 1::2] *= -1
+            b[torch.arange(128), torch.arange(128)] = amax
+            blocks.append(b)
+    return torch.cat(blocks).to(torch.bfloat16)
+
+
+def fp32_blocks(seed):
+    """Blocks [n, 128, 128] of fp32 values at the middles of two codes, and one step of fp32 to either side."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    table = torch.tensor(O.E4M3_MAGNITUDES, dtype=torch.float64, device="cuda")
+    n = 64
+    amax = (1 + torch.rand(n, 1, generator=g, device="cuda").double()).float()
+    amax[::4] = (amax[::4] * 16).round() / 16                  # few bits: many exact ties
+    amax[1::4] = amax[1::4].to(torch.bfloat16).float()
+    amax = amax * torch.exp2(torch.randint(-99, 127, (n, 1), generator=g, device="cuda").float())
+    i = torch.randint(0, 126, (n, 128 * 128), generator=g, device="cuda")
+    v = ((table[i] + table[i + 1]) / 2 * amax.double() / 448).float()
+    v = (v.contiguous().view(torch.int32) + torch.randint(-1, 2, v.shape, generator=g, device="cuda", dtype=torch.int32)).view(torch.float32)
+    v = torch.where(v.abs() <= amax, v, 0.0) * (1 - 2 * (i % 2))
+    v[:, 77] = amax[:, 0]
+    return v.view(n, 128, 128)
+
+
+def test_every_code_is_the_nearest(F):
+    """No tolerance: the quotient by the real amax / 448, ties to the even code, decided in exact arithmetic."""
+    x = bf16_blocks()
+    amax = x.double().abs().amax(1, keepdim=True)
+    q, _ = F.f8f8bf16_quantize_groupwise(x)
+    wrong = ~O.nearest(q, x.double(), amax)
+    assert not bool(wrong.any()), f"rows: {int(wrong.sum())} codes, first at {wrong.nonzero()[0].tolist()}"
+    w = x.view(-1, 128, 128).clone()
+    for at, t in (("bf16", w), ("fp32 of bf16", w.float())):
+        amax = t.double().abs().amax((1, 2), keepdim=True)
+        q = F.f8f8bf16_quantize_groupwise_weight(t).WQ
+        wrong = ~O.nearest(q, t.double(), amax)
+        assert not bool(wrong.any()), f"weights, {at}: {int(wrong.sum())} codes, first at {wrong.nonzero()[0].tolist()}"
+    for seed in range(8):
+        w = fp32_blocks(seed)
+        r = F.f8f8bf16_quantize_groupwise_weight(w, transposed=True)
+        wrong = ~O.nearest(r.WQ, w.double(), w.double().abs().amax((1, 2), keepdim=True))
+        assert not bool(wrong.any()), f"fp32 weights, seed {seed}: {int(wrong.sum())} codes, first at {wrong.nonzero()[0].tolist()}"
+
+
 def test_rows_agree_with_the_rowwise_quantiser(F):
     """One block per row: the codes of f8f8bf16_quantize_rowwise, but for values within rounding of a midpoint."""
     x = torch.randn(500, 128, device="cuda").to(torch.bfloat16)

@@ -67,6 +67,41 @@ def test_blocks():
     assert s.tolist()[0] == [1.0, 1.0] and math.isclose(float(s[1, 1]), 0.01) and math.isclose(float(q[1, 200]), 448.0)
 
 
+def test_nearest_against_fractions():
+    """Over single values in exact fractions, ties among them; and values on the wrong side of a middle are seen."""
+    from fractions import Fraction
+    table = [Fraction(m) for m in O.E4M3_MAGNITUDES]
+    assert float(table[126]) == 448 and float(table[1]) == 2.0 ** -9 and sorted(table) == table
+    g = torch.Generator().manual_seed(4)
+    amax = torch.randint(128, 256, (400,), generator=g).double() / 128
+    v = amax * 0 + torch.randint(-255, 256, (400,), generator=g).double() / 256 / torch.exp2(torch.randint(0, 12, (400,), generator=g).double())
+    ties = 0
+    for a, x in zip(amax.tolist(), v.tolist()):
+        q = abs(Fraction(x)) * 448 / Fraction(a)
+        off = [abs(q - t) for t in table]
+        best = [i for i in range(127) if off[i] == min(off)]
+        ties += len(best) > 1
+        want = min(best, key=lambda i: i % 2)
+        codes = torch.arange(256, dtype=torch.uint8)
+        ok = O.nearest(codes, torch.full((256,), x, dtype=torch.float64), torch.tensor(a, dtype=torch.float64))
+        signed = {want} | {want + 128} if want == 0 else {want + 128 * (x < 0)}
+        assert set(ok.nonzero().flatten().tolist()) == signed, (a, x)
+    assert ties
+
+
+def test_values_rounded_before_their_codes_are_seen():
+    """A code of v times the rounded 448 / amax, or of v over the rounded scale, is not always the nearest."""
+    g = torch.Generator().manual_seed(5)
+    amax = torch.randint(128, 256, (1 << 18,), generator=g).float() / 128
+    v = torch.randint(128, 256, (1 << 18,), generator=g).float() / 256
+    for q in (v * (448.0 / amax), v / (amax * (1.0 / 448.0)), v / (amax / 448.0)):
+        codes = q.to(torch.float8_e4m3fn).view(torch.uint8)
+        wrong = ~O.nearest(codes, v.double(), amax.double())
+        assert 0 < int(wrong.sum()) < 1 << 13
+    exact = (v.double() * 448 * 2.0 ** 40 / amax.double()).float() * 2.0 ** -40     # one rounding of the quotient: bf16's ties survive it
+    assert bool(O.nearest(exact.to(torch.float8_e4m3fn).view(torch.uint8), v.double(), amax.double()).all())
+
+
 def test_clip():
     a, b = torch.tensor([3.0]), torch.tensor([[0.0, 4.0]])
     norm, factor, out = O.clip([a, b], 1.0, 0.0)
