@@ -155,8 +155,8 @@ def offsets_of(w):
 
 
 # Sources that decide what the GEMM kernels do on a workload (kernels, selector,
-# shared header); the activation quantiser is built from its own file.
-GEMM_SOURCES = ("fp8gg_api.cpp", "fp8gg_internal.h", "fp8gg_kernels.hip")
+# headers they include); the activation quantiser is built from its own file.
+GEMM_SOURCES = ("fp8gg_api.cpp", "fp8gg_internal.h", "fp8gg_kernels.hip", "fp8gg_lds.h")
 
 
 def group_meta(w, layout):
