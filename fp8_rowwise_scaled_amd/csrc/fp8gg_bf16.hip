@@ -528,9 +528,12 @@ __global__ void __launch_bounds__(512, 2) product_persistent_kernel(ProductArgs 
 // groups, N = 1000, K = 7184, input's gradient: 70 us, 3.7 TB/s; 1536 in 16, N = K = 4096: 131 us, 4.3 TB/s): a tile's first
 // copies are under way before the last tile's output is stored, and these stores while it is computed.  Forward, groups start at
 // different places of the contraction: rows that lie a power of two apart and are read at the same place keep
-// only some of the memory's channels busy (256 rows in 32 groups, N = K = 2048: 61 -> 45 us; 1536 rows in 16,
-// N = K = 4096: 145 -> 131).  Different places for a group's own tiles gain less, as these share the rows of
-// its input (47, 146), and the input's gradient, whose reads run along the rows of W, nothing.
+// only some of the memory's channels busy.  Neighbouring groups, which are read at the same time, are five stages apart:
+// with one stage, 128 bytes, most of their reads still meet; 3, 5 and 7 are alike, and an odd number gives the groups as many
+// places as the contraction has (us for 0 / 1 / 3 / 5 / 7 stages, in a captured graph: 256 rows in 32 groups, N = K = 2048,
+// 67 / 48 / 49 / 49 / 49; 1536 in 16, N = K = 4096, 127 / 107 / 95 / 95 / 94; 1536 in 16, N = 7168, K = 2048, 106 / 99 / 92 / 91 / 90;
+// 1537 in 16, N = 1000, K = 7184, whose rows are not a power of two apart, 98 with any).  Different places for a group's own
+// tiles gain less, as these share the rows of its input, and the input's gradient, whose reads run along the rows of W, nothing.
 template <bool Q_ALONG>
 __global__ void __launch_bounds__(512, 2) product_stream_kernel(ProductArgs a) {
   constexpr int BM = 128, BN = 256, BK = 64;

@@ -35,8 +35,11 @@ extern "C" {
 /*
  * Products of bf16 matrices by group, in the stacked layout: group g owns the next
  * M_sizes[g] rows of X, Y, dX and dY.  Sums of products in fp32, rounded once (to nearest
- * even) where the output is bf16; the order of a sum's terms depends on the sizes of the
- * call and on the row's place in its group, never on the run.
+ * even) where the output is bf16.  The order of a sum's terms depends on G, total_M, N and K,
+ * in bf16_grouped_stacked also on the group's index (groups of few rows start at different
+ * places of the contraction), and on nothing else: at the same sizes a row of Y or dX has the
+ * same bits wherever it lies in its group and whatever the other rows and M_sizes are, and
+ * dW[g] depends on its group's rows and their order alone.
  *
  *     Y[m, n]  = sum_k X[m, k] W[g, n, k]              bf16_grouped_stacked
  *     dX[m, k] = sum_n dY[m, n] W[g, n, k]             bf16_grouped_stacked_dgrad

@@ -241,6 +241,43 @@ def test_results_do_not_depend_on_the_run(F):
         assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+# all three kernels of the rows' products, tiles whole, in halves and in quarters
+@pytest.mark.parametrize("G,M,N,K", [(3, 40, 136, 520), (24, 1500, 2056, 256), (20, 600, 1032, 4096), (2, 5000, 264, 2568), (3, 6000, 2312, 128), (9, 300, 1000, 264)])
+def test_a_row_has_the_same_bits_wherever_it_lies(F, G, M, N, K):
+    """At the same G, total_M, N and K: in another place of its group, among other rows and other groups' sizes.  The weights'
+    gradient of a group: whatever the other groups hold, and wherever its own rows start."""
+    print(f"case places G={G} M={M} N={N} K={K}", flush=True)
+    x, w, dy = inputs(G, M, N, K)
+    s = sizes_of(G, M, "even")
+    y, dx, dw = F.bf16_grouped_stacked(x, w, dev(s)), F.bf16_grouped_stacked_dgrad(dy, w, dev(s)), F.bf16_grouped_stacked_wgrad(dy, x, dev(s))
+    r = torch.Generator().manual_seed(M)
+    for seed in range(3):
+        other, _, dother = inputs(G, M, N, K, seed=20 + seed)
+        # groups take rows from their neighbours on one side and lose some to the other, by up to half their size
+        cut = [0]
+        for g in range(G - 1):
+            cut.append(min(M, max(cut[-1], sum(s[:g + 1]) + int(torch.randint(-(s[g] // 2), s[g] // 2 + 1, (1,), generator=r)))))
+        t = [b - a for a, b in zip(cut, cut[1:] + [M])]
+        rows = []                                         # (place now, place before) of the rows that are kept
+        for g in range(G):
+            n = min(s[g], t[g])
+            now, before = (torch.randperm(k, generator=r)[:n] for k in (t[g], s[g]))
+            rows.append(torch.stack([now + sum(t[:g]), before + sum(s[:g])]))
+        now, before = torch.cat(rows, 1).cuda()
+        other[now], dother[now] = x[before], dy[before]
+        for got, want in ((F.bf16_grouped_stacked(other, w, dev(t)), y), (F.bf16_grouped_stacked_dgrad(dother, w, dev(t)), dx)):
+            assert torch.equal(got[now].view(torch.int16), want[before].view(torch.int16))
+    # group g's rows as they are, further ahead: the first group has fewer, and the last rows are no group's
+    g = G // 2
+    t = [s[0] - s[0] // 3] + s[1:]
+    other, _, dother = inputs(G, M, N, K, seed=40)
+    a, b, n = sum(s[:g]), sum(t[:g]), s[g]
+    other[b:b + n], dother[b:b + n] = x[a:a + n], dy[a:a + n]
+    for dtype in (torch.float32, torch.bfloat16):
+        got = F.bf16_grouped_stacked_wgrad(dother, other, dev(t), dtype=dtype)
+        assert torch.equal(got[g], dw[g].to(dtype))
+
+
 @pytest.mark.parametrize("G,M,N,K", [(3, 4, 128, 256), (4, 120, 264, 136), (2, 900, 520, 328), (1, 6000, 64, 136)])
 def test_gradients_against_differences(F, G, M, N, K):
     """The gradients are those of the forward product: for a loss sum(dY * Y), which is linear in X and in
