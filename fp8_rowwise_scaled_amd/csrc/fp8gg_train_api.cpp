@@ -269,8 +269,9 @@ fp8gg_status f8f8bf16_quantize_groupwise_weight(const void* W, int w_dtype, uint
     return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "N=%lld and K=%lld must be multiples of 128", (long long)N, (long long)K);
   if ((WQt == nullptr) != (wt_scale == nullptr))
     return fail(FP8GG_ERR_INVALID_ARGUMENT, "WQt and wt_scale are given together or not at all");
+  // a workgroup of 256 threads per block, and a launch holds fewer than 2^32 threads
   const double blocks = (double)G * (N / 128) * (K / 128);
-  if (G > kMaxDim || N > kMaxDim || K > kMaxDim || blocks > 0x7FFFFFFF)
+  if (G > kMaxDim || N > kMaxDim || K > kMaxDim || blocks >= 1 << 24)
     return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "G=%lld N=%lld K=%lld is too large", (long long)G, (long long)N, (long long)K);
   if (blocks == 0) return ok();
   const int64_t n = G * N * K, scales = (int64_t)blocks * 4;

@@ -100,7 +100,8 @@ fp8gg_status f8f8bf16_quantize_groupwise(
  *   WQt       [G, K, N]               e4m3fn, WQt[g, k, n] = WQ[g, n, k]     (both or neither NULL)
  *   wt_scale  [G, K / 128, N / 128]   fp32
  *
- * N % 128 == 0, K % 128 == 0; W, WQ and WQt 16-byte aligned, fewer than 2^31 blocks.
+ * N % 128 == 0, K % 128 == 0; W, WQ and WQt 16-byte aligned, fewer than 2^24 blocks
+ * (2^38 values).
  */
 fp8gg_status f8f8bf16_quantize_groupwise_weight(
     const void* W, int w_dtype, uint8_t* WQ, float* w_scale, uint8_t* WQt, float* wt_scale,

@@ -95,6 +95,18 @@ def test_quantize_refusals():
     assert weight(G=0, w=None, q=None, s=None, qt=None, st=None) == OK
 
 
+def test_weight_blocks_refused_past_a_launch():
+    """A workgroup of 256 threads per block, and fewer than 2^32 threads in a launch."""
+    big = 1 << 50
+    def weight(N, K, G=1, t=True):
+        return lib().f8f8bf16_quantize_groupwise_weight(big, 0, 2 * big, A[0], 3 * big if t else None, A[1] if t else None, G, N, K, None)
+    for G, N, K in ((1, 128 << 12, 128 << 12), (1 << 24, 128, 128), (3, 128 << 12, 128 << 11)):
+        for t in (True, False):
+            assert weight(N, K, G, t) == SHAPE and "too large" in F.layer_last_error()
+    # one block fewer passes the checks (and meets the addresses' overlap)
+    assert weight(128, 128, (1 << 24) - 1) == BAD and "overlaps" in F.layer_last_error()
+
+
 def table(*tensors):
     """(grads, counts, dtypes, n) of (address, count, dtype) triples."""
     n = len(tensors)
