@@ -27,7 +27,7 @@ int compute_units() {
   return cus;
 }
 
-fp8gg_status check_product(int64_t G, int64_t M, int64_t N, int64_t K) {
+fp8gg_status check_product(int64_t G, int64_t M, int64_t N, int64_t K, int weight_size = 2) {
   if (G < 0 || M < 0 || N < 0 || K < 0)
     return fail(FP8GG_ERR_INVALID_ARGUMENT, "negative size (G=%lld total_M=%lld N=%lld K=%lld)", (long long)G, (long long)M,
                 (long long)N, (long long)K);
@@ -38,8 +38,8 @@ fp8gg_status check_product(int64_t G, int64_t M, int64_t N, int64_t K) {
     return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "G=%lld total_M=%lld N=%lld K=%lld is too large", (long long)G, (long long)M,
                 (long long)N, (long long)K);
   // tensors of at most 2^47 bytes
-  const double most = std::ldexp(1.0, 46);
-  if ((double)M * N > most || (double)M * K > most || (double)G * N * K > most)
+  const double most = std::ldexp(1.0, 47);
+  if ((double)M * N * 2 > most || (double)M * K * 2 > most || (double)G * N * K * weight_size > most)
     return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "a tensor of G=%lld total_M=%lld N=%lld K=%lld exceeds 2^47 bytes", (long long)G,
                 (long long)M, (long long)N, (long long)K);
   return FP8GG_OK;
@@ -223,9 +223,9 @@ int64_t bf16_grouped_stacked_wgrad_workspace(int64_t G, int64_t total_M, int64_t
 fp8gg_status bf16_grouped_stacked_wgrad(const uint16_t* dY, const uint16_t* X, const int64_t* M_sizes, void* dW, int dw_dtype,
                                         int accumulate, void* workspace, int64_t workspace_bytes, int64_t G, int64_t total_M,
                                         int64_t N, int64_t K, void* stream) {
-  FP8GG_TRY(check_product(G, total_M, N, K));
   FP8GG_TRY(check_float_type(dw_dtype, "dw_dtype"));
   const bool f32 = dw_dtype == FP8GG_DTYPE_F32;
+  FP8GG_TRY(check_product(G, total_M, N, K, f32 ? 4 : 2));
   if (accumulate && !f32) return fail(FP8GG_ERR_INVALID_ARGUMENT, "accumulate needs an fp32 dW");
   if (G == 0 || N == 0 || K == 0) return ok();
   const int64_t need = bf16_grouped_stacked_wgrad_workspace(G, total_M, N, K);

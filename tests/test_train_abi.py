@@ -71,6 +71,16 @@ def test_wgrad_refusals():
     assert call(G=1, M=8192, ws=A[3], size=need) == BAD and "overlaps" in F.layer_last_error()
 
 
+def test_fp32_weight_gradients_past_the_largest_tensor():
+    """2^47 bytes are 2^45 fp32 values."""
+    def call(dt, G):
+        return lib().bf16_grouped_stacked_wgrad(A[0], A[1], A[2], A[0], dt, 0, None, 0, G, 8, 1 << 22, 1 << 20, None)
+    assert call(1, 9) == SHAPE and "2^47" in F.layer_last_error()
+    assert call(1, 8) == BAD and "overlaps" in F.layer_last_error()          # passes the sizes' check
+    assert call(0, 16) == BAD and "overlaps" in F.layer_last_error()
+    assert call(0, 17) == SHAPE and "2^47" in F.layer_last_error()
+
+
 def test_wgrad_workspace():
     """Sums of parts only where a few tiles meet many rows, and never more than 32 of them."""
     ws = lib().bf16_grouped_stacked_wgrad_workspace
