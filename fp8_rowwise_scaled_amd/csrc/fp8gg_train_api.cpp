@@ -27,14 +27,16 @@ int compute_units() {
   return cus;
 }
 
+// N and K: the kernels' offsets within 256 rows have 32 bits.
+constexpr int64_t kMaxProductWidth = 1 << 22;
+
 fp8gg_status check_product(int64_t G, int64_t M, int64_t N, int64_t K, int weight_size = 2) {
   if (G < 0 || M < 0 || N < 0 || K < 0)
     return fail(FP8GG_ERR_INVALID_ARGUMENT, "negative size (G=%lld total_M=%lld N=%lld K=%lld)", (long long)G, (long long)M,
                 (long long)N, (long long)K);
   if (N % 8 != 0 || K % 8 != 0)
     return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "N=%lld and K=%lld must be multiples of 8", (long long)N, (long long)K);
-  // N and K: the kernels' offsets within 256 rows have 32 bits
-  if (G > kMaxDim || M > kMaxDim || N > (1 << 22) || K > (1 << 22))
+  if (G > kMaxDim || M > kMaxDim || N > kMaxProductWidth || K > kMaxProductWidth)
     return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "G=%lld total_M=%lld N=%lld K=%lld is too large", (long long)G, (long long)M,
                 (long long)N, (long long)K);
   // tensors of at most 2^47 bytes
@@ -216,6 +218,7 @@ fp8gg_status bf16_grouped_stacked_dgrad(const uint16_t* dY, const uint16_t* W, c
 }
 
 int64_t bf16_grouped_stacked_wgrad_workspace(int64_t G, int64_t total_M, int64_t N, int64_t K) {
+  if (G > kMaxDim || total_M > kMaxDim || N > kMaxProductWidth || K > kMaxProductWidth) return 0;
   const int64_t splits = wgrad_splits(G, total_M, N, K);
   return splits > 1 ? splits * G * N * K * 4 : 0;
 }

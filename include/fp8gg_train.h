@@ -54,7 +54,8 @@ extern "C" {
  *                           dW holds, else every element is written, zeros for a group
  *                           without rows
  *   workspace               bf16_grouped_stacked_wgrad_workspace(G, total_M, N, K) bytes
- *                           (often 0), 16-byte aligned; NULL when that is 0
+ *                           (often 0, and for sizes that the call refuses), 16-byte aligned;
+ *                           NULL when that is 0
  *
  * Rows at or beyond the groups' end are neither read nor written.  What a row or column
  * holds, infinities and NaN included, reaches only the results that depend on it.  An empty

@@ -4,6 +4,8 @@ dereferenced)."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -87,6 +89,15 @@ def test_wgrad_workspace():
     assert ws(8, 4096, 4096, 7168) == 0 and ws(1, 64, 128, 128) == 0 and ws(0, 64, 128, 128) == 0 and ws(1, 0, 128, 128) == 0
     assert ws(1, 1 << 20, 128, 128) == 32 * 128 * 128 * 4 and ws(-1, 5, 8, 8) == 0
     assert ws(1, 1024, 256, 128) == 4 * 256 * 128 * 4
+
+
+@pytest.mark.parametrize("sizes", [(1 << 32, 1 << 40, 1 << 40, 8), (1, 1 << 20, (1 << 63) - 1, 8), ((1 << 63) - 1,) * 4, (1, -(1 << 63), 8, 8),
+                                   (1 << 31, 1 << 30, 8, 8), (1, 1 << 31, 8, 8), (1, 4096, 1 << 23, 8), (1, 4096, 8, 1 << 23)])
+def test_wgrad_workspace_of_sizes_that_are_refused(sizes):
+    """0, in a process of its own: products of such sizes have wrapped to 0 and been divided by."""
+    code = f"from fp8_rowwise_scaled_amd import _lib; print(_lib.load().bf16_grouped_stacked_wgrad_workspace(*{sizes}))"
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=os.path.dirname(os.path.dirname(HEADER)), timeout=120)
+    assert (r.returncode, r.stdout.strip()) == (0, "0"), r.stderr
 
 
 def test_quantize_refusals():
