@@ -161,10 +161,11 @@ class Call {
   }
 
   // The next argument as a list or tuple of float32 or bf16 tensors of one device, each dense (in
-  // any order of its axes: every value is dealt with by itself).  None: nothing.
-  std::vector<const at::Tensor*> tensors(const char* what) {
+  // any order of its axes: every value is dealt with by itself).  None: nothing.  They are held for the
+  // call: a list may lose its tensors while a later argument becomes a number or the lock is given up.
+  std::vector<at::Tensor> tensors(const char* what) {
     PyObject* o = args_[at_++];
-    std::vector<const at::Tensor*> list;
+    std::vector<at::Tensor> list;
     if (o == Py_None) return list;
     if (!PyList_Check(o) && !PyTuple_Check(o)) refuse("%s must be a list or tuple of tensors", what);
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
@@ -177,9 +178,9 @@ class Call {
       if (x.scalar_type() != at::kFloat && x.scalar_type() != at::kBFloat16)
         refuse("%s[%zd] must be bfloat16 or float32, got %s", what, i, name_of(x.scalar_type()));
       if (!x.is_non_overlapping_and_dense()) refuse("%s[%zd] must be dense (a view with gaps or repeats is not)", what, i);
-      list.push_back(&x);
+      list.push_back(x);
     }
-    for (const at::Tensor* x : list) on_device(*x, what);
+    for (const at::Tensor& x : list) on_device(x, what);
     return list;
   }
   // For calls without any tensor: the current device.
@@ -672,14 +673,14 @@ struct Pointers {
   std::vector<void*> out;
   std::vector<int64_t> counts;
   std::vector<int32_t> dtypes;
-  explicit Pointers(const std::vector<const at::Tensor*>& list) {
+  explicit Pointers(const std::vector<at::Tensor>& list) {
     g.reserve(list.size());
     counts.reserve(list.size());
     dtypes.reserve(list.size());
-    for (const at::Tensor* t : list) {
-      g.push_back(t->numel() ? t->const_data_ptr() : nullptr);
-      counts.push_back(t->numel());
-      dtypes.push_back(t->scalar_type() == at::kFloat ? FP8GG_DTYPE_F32 : FP8GG_DTYPE_BF16);
+    for (const at::Tensor& t : list) {
+      g.push_back(t.numel() ? t.const_data_ptr() : nullptr);
+      counts.push_back(t.numel());
+      dtypes.push_back(t.scalar_type() == at::kFloat ? FP8GG_DTYPE_F32 : FP8GG_DTYPE_BF16);
     }
   }
 };
@@ -715,9 +716,9 @@ PyObject* grad_clip(PyObject* const* args, Py_ssize_t n) {
   Pointers p(list);
   p.out.reserve(list.size());
   for (size_t i = 0; i < list.size(); ++i) {
-    const at::Tensor& o = in_place ? *list[i] : *outs[i];
-    if (o.scalar_type() != list[i]->scalar_type() || !o.sizes().equals(list[i]->sizes()) ||
-        !o.strides().equals(list[i]->strides()))
+    const at::Tensor& o = in_place ? list[i] : outs[i];
+    if (o.scalar_type() != list[i].scalar_type() || !o.sizes().equals(list[i].sizes()) ||
+        !o.strides().equals(list[i].strides()))
       refuse("outs[%zu] must have the type, shape and strides of grads[%zu]", i, i);
     p.out.push_back(o.numel() ? o.data_ptr() : nullptr);
   }

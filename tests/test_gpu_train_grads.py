@@ -186,6 +186,31 @@ def test_more_than_31_bits_of_values(F):
     assert abs(float(g[-1]) - 0.6) < 0.002 and abs(float(g[5]) - 0.8) < 0.003 and int(g.count_nonzero()) == 2
 
 
+def test_a_list_that_loses_its_tensors_during_the_call(F):
+    """A bound that is turned into a number by the caller's code, which empties the list: the call has its tensors all the same."""
+    class Bound:
+        def __init__(self, *lists):
+            self.lists = lists
+
+        def __float__(self):
+            for x in self.lists:
+                x.clear()
+            return 0.5 * norm
+    kept = make([4096, 12345])
+    norm = math.sqrt(sum(float(g.double().square().sum()) for g in kept))
+    want = O.clip(kept, 0.5 * norm, 0.0)[2]
+    views = [torch.empty_like(g) for g in kept]
+    grads, outs = [g.clone() for g in kept], list(views)
+    got = F.f8f8bf16_grad_clip(grads, Bound(grads), eps=0.0, outs=outs)
+    assert grads == [] and abs(float(got) - norm) <= 1.01 * U * norm
+    grads = [g.clone() for g in kept]
+    held = list(grads)
+    F.f8f8bf16_grad_clip(grads, Bound(grads), eps=0.0)
+    for a, b, w in zip(views, held, want):
+        assert torch.equal(a, b)
+        assert bool(((a.double() - w).abs() <= 2.02 * U * w.abs() + (2.0 ** -8 * 1.001 * w.abs() if a.dtype is torch.bfloat16 else 0)).all())
+
+
 def test_results_do_not_depend_on_the_run(F):
     grads = make([1 << 22, 12345, 1 << 20])
     first = [float(F.f8f8bf16_grad_square_sum(grads)) for _ in range(4)]
