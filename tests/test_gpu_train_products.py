@@ -120,6 +120,76 @@ def test_products_in_rounds(F, G, M, N, K, how):
         assert out.untouched((~written).numpy()).all(), f"{name}: a row past the groups' end was written"
 
 
+# the weights' gradient likewise: the groups' tiles over several rounds, in every XCD's eighths from 64 tiles a group on,
+# of more groups than a wave has lanes
+@pytest.mark.parametrize("G,M,N,K", [(6, 3000, 2056, 2056), (70, 2100, 2056, 2056), (130, 3000, 1800, 2312), (3, 700, 5128, 1032), (70, 4100, 520, 776)])
+@pytest.mark.parametrize("how", ["even", "skewed", "one", "short", "wrong"])
+def test_wgrad_in_rounds(F, G, M, N, K, how):
+    print(f"case wgrad rounds G={G} M={M} N={N} K={K} {how}", flush=True)
+    from fp8_rowwise_scaled_amd import _lib
+    assert _lib.load().bf16_grouped_stacked_wgrad_workspace(G, M, N, K) == 0          # whole groups, no parts
+    x, _, dy = inputs(G, M, N, K, seed=7)
+    s = sizes_of(G, M, how)
+    want, size = O.wgrad(dy.double(), x.double(), s)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = P.Guarded((G, N, K), dtype)
+        F.bf16_grouped_stacked_wgrad(dy, x, dev(s), dW=out.t)
+        torch.cuda.synchronize()
+        out.check("wgrad")
+        check(out.t, want, size, M, dtype is torch.bfloat16, f"wgrad {dtype}")
+    out = P.Guarded((G, N, K), torch.float32)
+    held = torch.randn(G, N, K, device="cuda")
+    out.t.copy_(held)
+    for _ in range(2):                                    # twice over: two micro-batches
+        F.bf16_grouped_stacked_wgrad(dy, x, dev(s), dW=out.t, accumulate=True)
+    torch.cuda.synchronize()
+    out.check("wgrad accumulated")
+    check(out.t, 2 * want + held.double(), 2 * size + held.double().abs(), 2 * M, False, "wgrad accumulated")
+    for g, r in enumerate(O.group_rows(s, M)):
+        assert len(r) or torch.equal(out.t[g], held[g]), f"group {g} has no rows"
+
+
+def columns(n):
+    """Of 2^22: some at its start, across its middle and at its end; everything that a sum's order could move."""
+    return torch.cat([torch.arange(40), torch.arange(n // 2 - 30, n // 2 + 50), torch.arange(n - 300, n)]).cuda()
+
+
+@pytest.mark.parametrize("M,other", [(3, 16), (100, 64), (100, 264), (260, 264), (260, 8)])
+def test_the_widest_rows(F, M, other):
+    """N or K of 2^22, the most that the offsets of a tile's 256 rows hold in 32 bits.  A contraction that long has zeros but
+    in a few places, which add nothing and no rounding: its length counts as theirs."""
+    n = 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(M + other)
+    at = columns(n)
+    s = dev([M])
+    wide = torch.zeros(M, n, dtype=torch.bfloat16, device="cuda")
+    wide[:, at] = randn(g, M, len(at))
+    w = torch.zeros(1, other, n, dtype=torch.bfloat16, device="cuda")
+    w[0][:, at] = randn(g, other, len(at))
+    narrow = randn(g, M, other)
+    print(f"case widest rows M={M} other={other}", flush=True)
+    xs, ws, ns = wide[:, at].double(), w[0][:, at].double(), narrow.double()
+    y = F.bf16_grouped_stacked(wide, w, s)                              # K = 2^22
+    check(y, xs @ ws.T, xs.abs() @ ws.abs().T, len(at), True, "forward, K")
+    dx = F.bf16_grouped_stacked_dgrad(narrow, w, s)
+    check(dx[:, at], ns @ ws, ns.abs() @ ws.abs(), other, True, "dgrad, K")
+    assert int(dx.count_nonzero()) == int(dx[:, at].count_nonzero())
+    for dtype in (torch.float32, torch.bfloat16):
+        dw = F.bf16_grouped_stacked_wgrad(narrow, wide, s, dtype=dtype)[0]
+        check(dw[:, at], ns.T @ xs, ns.abs().T @ xs.abs(), M, dtype is torch.bfloat16, "wgrad, K")
+        assert int(dw.count_nonzero()) == int(dw[:, at].count_nonzero())
+    w = w.transpose(1, 2).contiguous()
+    y = F.bf16_grouped_stacked(narrow, w, s)                            # N = 2^22
+    check(y[:, at], ns @ ws, ns.abs() @ ws.abs(), other, True, "forward, N")
+    assert int(y.count_nonzero()) == int(y[:, at].count_nonzero())
+    dx = F.bf16_grouped_stacked_dgrad(wide, w, s)
+    check(dx, xs @ ws.T, xs.abs() @ ws.abs().T, len(at), True, "dgrad, N")
+    for dtype in (torch.float32, torch.bfloat16):
+        dw = F.bf16_grouped_stacked_wgrad(wide, narrow, s, dtype=dtype)[0]
+        check(dw[at], xs.T @ ns, xs.abs().T @ ns.abs(), M, dtype is torch.bfloat16, "wgrad, N")
+        assert int(dw.count_nonzero()) == int(dw[at].count_nonzero())
+
+
 @pytest.mark.parametrize("G,M,N,K", [(1, 12000, 128, 72), (2, 5003, 264, 136), (3, 40000, 8, 8)])
 def test_wgrad_in_parts(F, G, M, N, K):
     """Few tiles and many rows: the rows are split, also where a group has fewer than the others' parts."""
