@@ -14,7 +14,8 @@ Backward:  from the gradient of the layer's output to those of its input, of the
 Training:  ``train_step`` keeps fp32 weights, quantises them for the block-scaled products
            of both passes (or uses bf16 products instead), adds the weights' gradients up in
            fp32 over micro-batches with bf16 products, clips them by their common norm, and
-           updates the weights.
+           updates the weights.  With bf16 products nothing is in 8 bits: the gated activation
+           between them and its gradient are then torch's, from the bf16 rows kept.
 
 The router's own product (tokens x hidden x experts, small) is torch's.  ``main`` runs the
 layer on random data, compares it with the same layer in fp32 torch operations, and
@@ -128,6 +129,19 @@ def train_dgrad(dy, q, M_sizes):
     return F.bf16_grouped_stacked_dgrad(dy, q, M_sizes)
 
 
+def gated(h):
+    """silu(gate) * up of bf16 rows [gate | up], in fp32, rounded once."""
+    gate, up = h.float().chunk(2, 1)
+    return (torch.nn.functional.silu(gate) * up).to(torch.bfloat16)
+
+
+def gated_backward(da, h):
+    """Its gradient from the rows themselves."""
+    gate, up = h.float().chunk(2, 1)
+    sig, d = torch.sigmoid(gate), da.float()
+    return torch.cat([d * up * sig * (1 + gate * (1 - sig)), d * gate * sig], 1).to(torch.bfloat16)
+
+
 def train_forward(x, residual, w: Weights, q: dict, k: int):
     """forward with the operands of train_operands: hidden and inner sizes that are multiples of 128."""
     norm = F.f8f8bf16_rmsnorm_quantize(x, w.norm, residual=residual, block=128, want_y=True, want_rstd=True)
@@ -136,8 +150,11 @@ def train_forward(x, residual, w: Weights, q: dict, k: int):
     rows = F.f8f8bf16_moe_dispatch(norm.XQ, norm.x_scale, route.dst_row)
     xb, _ = F.f8f8bf16_moe_combine_backward(norm.Y, route.dst_row)       # the same rows in bf16
     h = train_product(rows, xb, q["w1"], route.M_sizes)
-    act = F.f8f8bf16_silu_mul_quantize(h, block=128, checkpoint=True)
-    ab = (act.AQ.view(torch.float8_e4m3fn).float().unflatten(1, (-1, 128)) * act.a_scale[:, :, None]).flatten(1).to(torch.bfloat16)
+    if isinstance(q["w2"], F.WeightBlocks):
+        act = F.f8f8bf16_silu_mul_quantize(h, block=128, checkpoint=True)
+        ab = (act.AQ.view(torch.float8_e4m3fn).float().unflatten(1, (-1, 128)) * act.a_scale[:, :, None]).flatten(1).to(torch.bfloat16)
+    else:
+        act, ab = h, gated(h)
     y = train_product(act, ab, q["w2"], route.M_sizes)
     out = F.f8f8bf16_moe_combine(y, route.dst_row, route.weights)
     return out, norm.residual, (norm, logits, route, xb, act, ab, y)
@@ -150,7 +167,7 @@ def train_backward(dout, dresidual, w: Weights, q: dict, kept, grads: dict):
     dy, dweights = F.f8f8bf16_moe_combine_backward(dout, route.dst_row, route.weights, y)
     da = train_dgrad(dy, q["w2"], M)
     F.bf16_grouped_stacked_wgrad(dy, ab, M, dW=grads["w2"], accumulate=True)
-    dh = F.f8f8bf16_silu_mul_backward(da, act.HQ, act.h_scale)
+    dh = gated_backward(da, act) if torch.is_tensor(act) else F.f8f8bf16_silu_mul_backward(da, act.HQ, act.h_scale)
     drows = train_dgrad(dh, q["w1"], M)
     F.bf16_grouped_stacked_wgrad(dh, xb, M, dW=grads["w1"], accumulate=True)
     dlogits = F.f8f8bf16_route_backward(logits, route.ids, dweights, score="sigmoid")

@@ -3,7 +3,8 @@
  * layer (MI355X, gfx950): the products by group in bf16 with both gradients, the operands of
  * the block-scaled products, and the norm of all gradients with their clipping.
  *
- * A training step of a layer kept in bf16:
+ * A training step of a layer kept in bf16 (the gated activation between its products is the
+ * caller's: fp8gg_layer.h has it for 8-bit operands only):
  *
  *     grouped_stacked -> ... -> grouped_stacked_dgrad, grouped_stacked_wgrad -> grad_clip
  *
@@ -54,8 +55,8 @@ extern "C" {
  *                           dW holds, else every element is written, zeros for a group
  *                           without rows
  *   workspace               bf16_grouped_stacked_wgrad_workspace(G, total_M, N, K) bytes
- *                           (often 0, and for sizes that the call refuses), 16-byte aligned;
- *                           NULL when that is 0
+ *                           (often 0, and for negative sizes or those past the bounds below),
+ *                           16-byte aligned; NULL when that is 0
  *
  * Rows at or beyond the groups' end are neither read nor written.  What a row or column
  * holds, infinities and NaN included, reaches only the results that depend on it.  An empty
