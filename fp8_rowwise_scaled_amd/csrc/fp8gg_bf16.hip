@@ -10,11 +10,13 @@
 // transposed copy of anything is made.  v_mfma_f32_16x16x32_bf16 with the output's columns as its rows,
 // fp32 accumulators; tiles go global -> LDS without registers.
 //
-// What bounds it: on data as it comes the card's power.  A product of 4096 x 4096 x 7168 takes 126 us
-// on zeros and 161 on normal values (2.4 GHz against about 1.9), so what moves fewer bits counts as
-// much as what waits less: 16 x 16 x 32 instead of 32 x 32 x 16 instructions, which write half the sums per
-// product, 198 -> 176 us; copies addressed by a scalar base and a fixed offset per lane (no vector
-// arithmetic in the loop), 169 -> 164; neighbouring instructions that share an operand, 164 -> 163.
+// What bounds it: on data as it comes the card's power.  A product of 4096 x 4096 x 7168 in one group takes
+// 129 us on zeros and 168 on normal values (a library's product 110 and 151; each alone, in a captured graph;
+// in turn with others 141 and 176 against 118 and 158), so what moves fewer bits counts as much as what waits
+// less.  Steps on the way, each timed against the one before: 16 x 16 x 32 instead of 32 x 32 x 16
+// instructions, which write half the sums per product, 198 -> 176 us; copies addressed by a scalar base and a
+// fixed offset per lane (no vector arithmetic in the loop), 169 -> 164; neighbouring instructions that share an
+// operand, 164 -> 163.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -122,7 +124,7 @@ __device__ __forceinline__ uint32_t xcd_slot32(uint32_t w, uint32_t P) {
 
 // Tiles of a rows x cols grid in strips of four rows, column by column: the 32 tiles that an XCD works on
 // at a time are four rows by eight columns (12 panels of the operands to read), not one row or two
-// (18 to 30).  Input's gradient of 4096 rows in 8 groups, N = 4096, K = 7168: 234 -> 206 us.
+// (18 to 30).  Input's gradient of 4096 rows in 8 even groups, N = 4096, K = 7168: 225 us in strips of one row, 218 of four.
 __device__ __forceinline__ void in_strips(uint32_t tile, uint32_t rows, uint32_t cols, uint32_t& row, uint32_t& col) {
   constexpr uint32_t H = 4;
   const uint32_t strip = tile / (H * cols), at = tile - strip * H * cols, left = rows - strip * H, h = left < H ? left : H;
@@ -169,8 +171,10 @@ struct Operand {
   const uint8_t* base;           // of the tile's part of the operand, the same in all lanes
   uint32_t off[LOADS];           // this lane's chunks from there, in bytes
 
-  // 16-byte chunk c of LDS row `row` lies at c ^ swz(row): no bank conflicts in either kind of read
-  // (across: the four places that sixteen lanes read lie in four different 64-byte columns).
+  // 16-byte chunk c of LDS row `row` lies at c ^ swz(row): sixteen lanes meet no bank twice in either kind of
+  // read (across: the four places that they read lie in four different 64-byte columns; lanes that are read with
+  // them do meet theirs, as the counter of bank conflicts has 1% of the cycles of LDS in kernels that read along and
+  // 30 to 46% where an operand is read across).
   static __device__ __forceinline__ int swz(int row) {
     if constexpr (ALONG) return lds_swz<BK * 2>(row);
     else if constexpr (R >= 128) return (row & 3) << 2;
@@ -409,8 +413,7 @@ struct ProductTile {
 
   // The same while the HEAD of the next tile's prologue is under way, through the rest of the ring (Q's last two
   // slots), as many rows at a time as that holds.  Whole rows count: each wave by itself, without barriers but
-  // 256 bytes of a row at a time, takes 357 us instead of 342 for the gate and up weights' gradient, and
-  // straight from the registers, 64 bytes at a time, it took 366 instead of 309.  F32: the output's type, else
+  // 256 bytes of a row at a time, takes 357 us instead of 342 for the gate and up weights' gradient.  F32: the output's type, else
   // bf16.  What lies outside is sent past the buffer's end, which drops it, so that every wave issues the same
   // number of stores, STORES.
   template <bool F32>
@@ -481,9 +484,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, uint8_t* smem
 
 // One workgroup per compute unit: rounds of whole tiles, and the tiles that do not fill one as halves or
 // quarters where the rounds of these take less.  The matrix units under the power limit are the bound:
-// 4096 rows in 8 groups from 0 to 1400, N = 4096, K = 7168, forward 253 us (950 TFLOP/s; 50% of the cycles of
-// the matrix units busy, the rest mostly rows that tiles of 256 have and groups do not, and the last round),
-// input's gradient 245; one group of 4096 rows 163 us (1480 TFLOP/s, a library's product 159).
+// 4096 rows in 8 groups from 0 to 1400, N = 4096, K = 7168, forward 252 us (950 TFLOP/s; 52% of the cycles of
+// the matrix units busy, the rest mostly rows that tiles of 256 have and groups do not, and the last round), input's gradient 245; in 8 even groups 194 and 212;
+// in one group 168 to 184 (1310 to 1430 TFLOP/s; a library's product in turn 151 to 164).
 template <bool Q_ALONG>
 __global__ void __launch_bounds__(512, 2) product_persistent_kernel(ProductArgs a) {
   constexpr int BM = 256, BN = 256;
@@ -496,9 +499,10 @@ __global__ void __launch_bounds__(512, 2) product_persistent_kernel(ProductArgs 
   const RowTiles n = count_row_tiles<BM>(a);
   const uint32_t T = n.all * a.col_tiles, tall = n.tall * a.col_tiles;
   // Rounds of whole tiles: as many as the tall ones fill, as all fill, or all.  Of the tiles behind them the tall
-  // ones have two halves, the others one.  A round of halves takes 0.6 of one of whole tiles, of quarters 0.4
-  // (4096 rows in one group, N = 2048, K = 4096, whose 128 tiles fill half a round: 96 us whole, 58 as halves,
-  // 73 as two rounds of quarters).
+  // ones have two halves, the others one.  A round of halves counts as 0.6 of one of whole tiles, of quarters as 0.4
+  // (4096 rows in one group, N = 2048, K = 4096, whose 128 tiles fill half a round: 100 us whole, 68 to 70 as halves,
+  // 83 as two rounds of quarters; 4096 rows in 8 groups from 0 to 1400, N = 4096, K = 7168: 335, 292, 258 forward and
+  // 300, 256, 262 for the input's gradient).
   uint32_t whole = T, rest = 0, halves = 0, parts = 1, least = (T + P - 1) / P * 10;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -525,7 +529,8 @@ __global__ void __launch_bounds__(512, 2) product_persistent_kernel(ProductArgs 
 }
 
 // The same with tiles of half the rows, for groups whose weights' way from memory is the bound (1537 rows in 16
-// groups, N = 1000, K = 7184, input's gradient: 70 us, 3.7 TB/s; 1536 in 16, N = K = 4096: 131 us, 4.3 TB/s): a tile's first
+// uneven groups, N = 1000, K = 7184, input's gradient: 70 us, 3.7 TB/s; 1536 in 16, N = K = 4096: 130 us, 4.3 TB/s, in even
+// groups 95, 5.9 TB/s): a tile's first
 // copies are under way before the last tile's output is stored, and these stores while it is computed.  Forward, groups start at
 // different places of the contraction: rows that lie a power of two apart and are read at the same place keep
 // only some of the memory's channels busy.  Neighbouring groups, which are read at the same time, are five stages apart:
@@ -590,7 +595,8 @@ __global__ void __launch_bounds__(512, 2) product_stream_kernel(ProductArgs a) {
   }
 }
 
-// Few tiles: latency is the bound, and the bytes that are under way at a time.  The W waves of a workgroup take a part of the contraction each, in rings of their own,
+// Few tiles: latency is the bound, and the bytes that are under way at a time (one row, N = 7168, K = 2048, forward 8.0 us,
+// of which 3 a launch's; 29 MB).  The W waves of a workgroup take a part of the contraction each, in rings of their own,
 // and their sums are added in the order of the waves.
 template <bool Q_ALONG, int BN, int BK, int W, int SLOTS>
 __global__ void __launch_bounds__(W * 64) product_split_kernel(ProductArgs a) {
@@ -692,8 +698,9 @@ struct GroupTable {
 // the groups one after the other, the largest first.  A tile's first copies are under way before the last
 // tile's sums are stored, and these stores while it is computed: 6143 rows in 64 groups, N = 1024, K = 1536, bf16
 // 60 us against 75 with a workgroup per tile (201 MB out; 46 us at a copy's rate).  8 groups of 4096 rows in all,
-// N = 4096, K = 7168, fp32 343 us: the stores alone take 185 (940 MB), the products alone 189, and a wave waits
-// for its stores before the copies behind them, which the counter of both reports in order.
+// N = 4096, K = 7168, fp32 343 to 350 us: the stores alone take 185 (940 MB), the products alone 189, and a wave waits
+// for its stores before the copies behind them, which the counter of both reports in order.  Added to what dW holds:
+// 565 us (1.97 GB, 390 at a copy's rate), as each old value is waited for behind the stores before it.
 // a.splits > 1: the group's rows in so many parts, each part's sums to a.partial.
 template <bool F32>
 __global__ void __launch_bounds__(512, 2) wgrad_kernel(ProductArgs a) {
@@ -800,14 +807,16 @@ int64_t most_row_tiles(const ProductArgs& a, int64_t BM) { return a.M / BM + (a.
 
 enum Variant { kSplit, kStream, kPersistent };
 
-// Few tiles of 32 x 128 leave compute units idle unless the contraction is split (8 to 256 such tiles, us split
-// and by tiles of 128 x 256: one row of 4096 x 7168, 13 / 49 forward, 16 / 31 input's gradient; 128 rows in 2
-// groups, N = 2048, K = 4096, 18 / 32 and 20 / 19; 24 rows in 4, N = 4096, K = 2048, 16 / 22 and 17 / 33; 16 in 8,
-// N = 4096, K = 7168, 60 / 66 forward).  Groups of few rows are bound by the weights' way from memory, which tiles
-// of 128 rows with their stores behind the next tile keep busiest; large ones by the matrix units, which tiles of
-// 256 x 256 feed with half the reads (us at 128 / 256 rows: 8 groups of 512, N = 4096, K = 7168, 288 / 254;
-// 8 of 350, N = 4096, K = 2048, 75 / 62 for the input's gradient; 8 of 187, N = K = 4096, 76 / 76; 16 of 156,
-// N = K = 2048, 41 / 43).
+// By the sizes that the host knows: the rows of an average group.  Few tiles of 32 x 128 leave compute units idle unless
+// the contraction is split (us in captured graphs, even groups, split and by tiles of 128 x 256: one row of 4096 x 7168,
+// 17 / 56 forward, 23 / 38 input's gradient; 128 rows in 2 groups, N = 2048, K = 4096, 14 / 36 and 16 / 23; 24 rows in 4,
+// N = 4096, K = 2048, 20 / 22 and 23 / 39; 16 in 8, N = 4096, K = 7168, 86 / 83 forward, N = 7168, K = 2048, 53 / 66 input's
+// gradient; with more such tiles, 16 in 8, N = 7168, K = 2048 forward, 57 / 45).  Uneven groups: 68 and 60 rows,
+// N = 2048, K = 4096, 24 / 36 and 25 / 24.  Groups of few rows are bound by the weights' way from memory, which tiles of
+// 128 rows with their stores behind the next tile keep busiest; large ones by the matrix units, which tiles of 256 x 256
+// feed with half the reads (at 128 / 256 rows, forward and input's gradient: 8 groups of 512, N = 4096, K = 7168, 237 / 201
+// and 252 / 217; 8 of 350, N = 4096, K = 2048, 64 / 66 and 67 / 70, uneven 78 / 64 and 73 / 70; 8 of 187, N = K = 4096,
+// 86 / 81 and 93 / 79; 16 of 156, N = K = 2048, 46 / 44 forward, uneven 41 / 43; 16 of 96, N = K = 4096, 96 / 127 forward).
 Variant variant_of(const ProductArgs& a) {
   if (most_row_tiles(a, 32) * cdiv(a.C, 128) <= 256) return kSplit;
   return a.M / a.G < 192 ? kStream : kPersistent;
@@ -848,7 +857,9 @@ hipError_t launch_product(bool transposed, ProductArgs a, int cus, hipStream_t s
 }
 
 // A group's rows in parts where its tiles do not fill the compute units: up to two tiles for each, of 256 rows
-// at least (below, the parts' sums cost more than they gain), and no more than 32 partial sums a value.
+// at least, and no more than 32 partial sums a value.  Fewer rows cost more for the parts' sums than they gain (us with
+// parts of 128 / 256 / 512 rows at least: 256 rows in one group, N = K = 1024, 19 / 15 / 15; 1024 in 4, 31 / 16 / 16; 4096
+// in 4, 66 / 42 / 35); more leave units idle where there is one tile (1024 rows, N = K = 256, 19 / 19 / 23).
 int wgrad_splits(int64_t G, int64_t M, int64_t N, int64_t K) {
   if (G <= 0 || M <= 0 || N <= 0 || K <= 0) return 1;
   const int64_t tiles = G * cdiv(N, kWgradRows) * cdiv(K, kWgradCols);

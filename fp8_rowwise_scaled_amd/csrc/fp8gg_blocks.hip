@@ -43,7 +43,7 @@ struct Inverse {
 // A row is a whole number of blocks, so the tensor is one run of blocks of 128 values (256 bytes),
 // and block b's scale is x_scale[b].  Eight lanes take a block, sixteen values each: 32 bytes in, 16 out, and three
 // swaps within the eight for the largest magnitude.  Memory is the bound: 16383 x 4096 in 34 us, 5.9 TB/s
-// (a 1 GiB copy reaches 5.0); 64 x 7168 in 2.4 us, a launch's latency.  Inputs beyond the caches are read
+// (a 1 GiB copy reaches 5.1 to 5.2); 64 x 7168 in 2.4 us, a launch's latency.  Inputs beyond the caches are read
 // past them.
 
 constexpr int kRowsThreads = 256;
@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kRowsThreads) quantize_groupwise_kernel(const 
 // codes.  Four rows' codes of four columns, a word each, turn into four columns' codes of four rows
 // by byte permutations, so a thread has sixteen neighbouring bytes of the transposed block for each
 // of its columns; the block is put together in LDS, whose row q * 32 + c holds column 4 c + q and
-// whose 16-byte chunks are swapped by c, which keeps both accesses free of bank conflicts.  Memory is the bound: fp32 of
-// 8 x 4096 x 7168 to both orders in 245 us, 5.75 TB/s (1.41 GB; reading the block again for the transposed
+// whose 16-byte chunks are swapped by c, so that sixteen neighbouring lanes meet no bank twice.  Memory is the bound: fp32 of
+// 8 x 4096 x 7168 to both orders in 247 us, 5.7 TB/s (1.41 GB; reading the block again for the transposed
 // order would be 0.94 GB more).
 
 constexpr int kWeightThreads = 256;

@@ -7,7 +7,7 @@
 // workgroup's sum goes to a place of its own and these are added in a fixed order: results are
 // the same on every run.
 //
-// Memory is the bound: 291 million values of both types, norm and clipping into other tensors, in 590 us (5.5 TB/s
+// Memory is the bound: 270 million values of both types, norm and clipping into other tensors, in 596 us (5.4 TB/s
 // over two reads and a write); the additions in fp64 are hidden behind the loads.  A million values in 12 tensors
 // take 10 us, two launches of 3 us that wait for one another: every workgroup of the second adds up the first's
 // sums, since one more launch between them costs as much as either.
