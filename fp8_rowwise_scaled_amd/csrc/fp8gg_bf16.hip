@@ -172,9 +172,9 @@ struct Operand {
   uint32_t off[LOADS];           // this lane's chunks from there, in bytes
 
   // 16-byte chunk c of LDS row `row` lies at c ^ swz(row): sixteen lanes meet no bank twice in either kind of
-  // read (across: the four places that they read lie in four different 64-byte columns; lanes that are read with
-  // them do meet theirs, as the counter of bank conflicts has 1% of the cycles of LDS in kernels that read along and
-  // 30 to 46% where an operand is read across).
+  // read (across: the four places that they read lie in four different 64-byte columns.  Others read with them
+  // may meet theirs: the counter of bank conflicts has 1% of the cycles of LDS in kernels that read along, 30 to 46% where
+  // an operand is read across).
   static __device__ __forceinline__ int swz(int row) {
     if constexpr (ALONG) return lds_swz<BK * 2>(row);
     else if constexpr (R >= 128) return (row & 3) << 2;
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(512, 2) product_stream_kernel(ProductArgs a) {
   }
 }
 
-// Few tiles: latency is the bound, and the bytes that are under way at a time (one row, N = 7168, K = 2048, forward 8.0 us,
+// Few tiles: latency is the bound, and the bytes that are under way at a time (one row, N = 7168, K = 2048, forward 8.1 us,
 // of which 3 a launch's; 29 MB).  The W waves of a workgroup take a part of the contraction each, in rings of their own,
 // and their sums are added in the order of the waves.
 template <bool Q_ALONG, int BN, int BK, int W, int SLOTS>
