@@ -71,7 +71,9 @@ fp8gg_status check_grads(const Grads& s) {
     if (s.dtypes[i] != FP8GG_DTYPE_BF16 && s.dtypes[i] != FP8GG_DTYPE_F32)
       return fail(FP8GG_ERR_INVALID_ARGUMENT, "dtypes[%lld]=%d must be bf16 (0) or fp32 (1)", (long long)i, s.dtypes[i]);
     if (s.counts[i] < 0) return fail(FP8GG_ERR_INVALID_ARGUMENT, "counts[%lld] is negative", (long long)i);
-    if (s.counts[i] > (int64_t(1) << 44)) return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "counts[%lld] is too large", (long long)i);
+    // the chunks of a launch's tensors are counted in 32 bits (366 GB a tensor)
+    if (s.counts[i] > 0x7FFFFFFF / kGradTensors * (int64_t)(kGradChunk / s.size(i)))
+      return fail(FP8GG_ERR_UNSUPPORTED_SHAPE, "counts[%lld] is too large", (long long)i);
     if (s.counts[i] == 0) continue;
     if (!s.g[i]) return fail(FP8GG_ERR_INVALID_ARGUMENT, "grads[%lld] is null", (long long)i);
     if ((uintptr_t)s.g[i] % s.size(i)) return fail(FP8GG_ERR_INVALID_ARGUMENT, "grads[%lld] is not aligned to its type", (long long)i);
@@ -129,7 +131,7 @@ fp8gg_status check_outs(const Grads& s) {
   return FP8GG_OK;
 }
 
-// Calls f on the tensors in launches of kGradTensors at most (also where their chunks would pass 32 bits).
+// Calls f on the tensors in launches of kGradTensors at most.
 template <typename F>
 fp8gg_status for_each_launch(const Grads& s, F f) {
   GradArgs a;
@@ -137,14 +139,13 @@ fp8gg_status for_each_launch(const Grads& s, F f) {
   a.chunks = 0;
   for (int64_t i = 0; i < s.n; ++i) {
     if (s.counts[i] == 0) continue;
-    const int64_t chunks = grad_chunks(s.g[i], s.counts[i], s.size(i));
-    if (a.tensors == kGradTensors || a.chunks + chunks > 0x7FFFFFFFLL) {
+    if (a.tensors == kGradTensors) {
       FP8GG_TRY(f(a));
       a.tensors = 0;
       a.chunks = 0;
     }
     a.t[a.tensors++] = {s.g[i], s.out ? s.out[i] : nullptr, s.counts[i], a.chunks, s.dtypes[i] == FP8GG_DTYPE_F32};
-    a.chunks += (uint32_t)chunks;
+    a.chunks += (uint32_t)grad_chunks(s.g[i], s.counts[i], s.size(i));
   }
   return a.tensors ? f(a) : FP8GG_OK;
 }

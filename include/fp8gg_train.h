@@ -118,7 +118,8 @@ fp8gg_status f8f8bf16_quantize_groupwise_weight(
  *     factor     = min(1, max_norm / (norm + eps));  1 where max_norm is infinite or norm + eps is 0
  *
  *   grads, outs   n device pointers each, in host memory: bf16 or fp32 tensors (dtypes),
- *                 counts[i] values, aligned to their type; an empty tensor's may be NULL.
+ *                 counts[i] values (366 GB at most), aligned to their type; an empty tensor's
+ *                 may be NULL.
  *                 outs[i] may be grads[i] (the whole of it); nothing is written there when
  *                 the factor is 1.  The arrays are read before the call returns.
  *   square_sum    [1] fp64: grad_square_sum writes it; grad_clip takes it where it is given

@@ -152,6 +152,17 @@ def test_square_sum_refusals():
     assert lib().f8f8bf16_grad_square_sum(None, None, None, 1, A[8], A[9], 1 << 20, None) == BAD
 
 
+@pytest.mark.parametrize("dtype,most", [(1, (0x7FFFFFFF // 96) * 4096), (0, (0x7FFFFFFF // 96) * 8192)])
+def test_gradients_past_a_launch(dtype, most):
+    """96 tensors' chunks of 16 KB are counted in 32 bits: tensors of more than 366 GB are refused (they wrapped the count)."""
+    def call(count):
+        g, c, d, n = table((A[0], count, dtype))
+        return lib().f8f8bf16_grad_square_sum(g, c, d, n, A[0], A[9], 1 << 20, None)
+    assert call(most) == BAD and "square_sum overlaps grads[0]" in F.layer_last_error()     # passes the sizes' check
+    for count in (most + 1, 1 << 43, (1 << 44) - 1, 1 << 44, (1 << 63) - 1):
+        assert call(count) == SHAPE and "counts[0]" in F.layer_last_error(), count
+
+
 def test_clip_refusals():
     def call(*tensors, outs=None, sum_=None, bound=1.0, eps=0.0, norm=A[8], ws=A[9], size=1 << 20):
         g, c, d, n = table(*tensors)
